@@ -25,7 +25,10 @@ GPTQ_FACTOR_R_FORM = 2  # R = U^-1 and U's 128 x 128 diagonal blocks, for gptq_q
 GPTQ_GRID_SYMMETRIC = 0
 GPTQ_GRID_ASYMMETRIC = 1
 
-# every symbol the header declares, with its ctypes signature
+GPTQ_MX_E2M1 = 0  # MX elements of 4 bits
+GPTQ_MX_E4M3 = 1  # MX elements of 8 bits
+
+# every symbol the headers declare, with its ctypes signature
 _c_int64 = ctypes.c_int64
 _vp = ctypes.c_void_p
 SIGNATURES = {
@@ -55,6 +58,24 @@ SIGNATURES = {
     "gptq_dequant_matmul": (ctypes.c_int, [_vp, ctypes.c_int, _c_int64, _c_int64, _c_int64, _vp, _vp, _vp, _vp,
                                            _c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp, ctypes.c_int,
                                            _vp, _c_int64, _vp]),
+    "gptq_mx_code_bytes_per_row": (_c_int64, [_c_int64, ctypes.c_int]),
+    "gptq_mx_scale_bytes_per_row": (_c_int64, [_c_int64]),
+    "gptq_mx_quantize": (ctypes.c_int, [_vp, ctypes.c_int, _c_int64, _c_int64, _c_int64, ctypes.c_int, _vp, _vp, _vp]),
+    "gptq_mx_dequantize": (ctypes.c_int, [_vp, _vp, ctypes.c_int, _c_int64, _c_int64, _vp, ctypes.c_int, _c_int64,
+                                          _vp]),
+    "gptq_mx_matmul_workspace_bytes": (ctypes.c_size_t, [_c_int64, _c_int64, _c_int64, ctypes.c_int]),
+    "gptq_mx_matmul": (ctypes.c_int, [_vp, _vp, ctypes.c_int, _c_int64, _c_int64, _vp, _vp, _c_int64, _vp,
+                                      ctypes.c_int, _vp, ctypes.c_int, _c_int64, _vp, ctypes.c_size_t, _vp]),
+    "gptq_mx_linear_workspace_bytes": (ctypes.c_size_t, [_c_int64, _c_int64, _c_int64, ctypes.c_int]),
+    "gptq_mx_linear": (ctypes.c_int, [_vp, ctypes.c_int, _c_int64, _c_int64, _c_int64, ctypes.c_int, _vp, _vp,
+                                      _c_int64, _vp, ctypes.c_int, _vp, ctypes.c_int, _c_int64, _vp, ctypes.c_size_t,
+                                      _vp]),
+    "gptq_mx_grad_input_workspace_bytes": (ctypes.c_size_t, [_c_int64, _c_int64, _c_int64]),
+    "gptq_mx_grad_input": (ctypes.c_int, [_vp, _c_int64, _c_int64, _c_int64, _vp, _vp, _c_int64, _vp, _vp,
+                                          ctypes.c_int, _vp, ctypes.c_int, _c_int64, _vp, ctypes.c_size_t, _vp]),
+    "gptq_mx_grad_weight_workspace_bytes": (ctypes.c_size_t, [_c_int64, _c_int64, _c_int64]),
+    "gptq_mx_grad_weight": (ctypes.c_int, [_vp, _c_int64, _c_int64, _c_int64, _vp, _vp, ctypes.c_int, _c_int64,
+                                           ctypes.c_int, _vp, ctypes.c_int, _c_int64, _vp, _vp, ctypes.c_size_t, _vp]),
 }
 
 _lib = None
