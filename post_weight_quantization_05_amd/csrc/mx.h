@@ -11,6 +11,11 @@ constexpr int MX_BLOCK = 32;  // columns that share a scale
 static inline int64_t mx_code_row(int64_t cols, int fmt) { return ceil_div(cols, 128) * (fmt == GPTQ_MX_E2M1 ? 64 : 128); }
 static inline int64_t mx_scale_row(int64_t cols) { return ceil_div(cols, 512) * 16; }
 
+// every row of p starts at a 16-byte aligned address
+static inline bool vec_rows(const void* p, int64_t ld, int dtype) {
+  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * (dtype == GPTQ_F32 ? 4 : 2)) % 16 == 0;
+}
+
 // One MX operand: rows of codes and scales at their fixed row lengths.
 struct MxMatrix {
   const uint8_t* codes;

@@ -2,117 +2,161 @@
 // instructions of gfx950: v_mfma_scale_f32_32x32x64_f8f6f4 multiplies 4- and 8-bit elements and applies each
 // block's two scale bytes to its 32 products before they are added in fp32.
 //
-// Simple form: a wave forms 32 x 32 of Y, its lanes loading their own elements of each 64-column step. W is the
-// first operand, so that a lane of the result holds four consecutive columns of Y.
-//
-// Lane l = 32 h + r of an operand holds row r: 4-bit elements of columns 32 h .. 32 h + 31 of the 64; 8-bit
-// elements of columns 16 h .. 16 h + 15 and 32 + 16 h .. 32 + 16 h + 15; in both cases the scale byte of block h.
+// W is the first operand, so that a lane of the result holds four consecutive columns of Y. Lane l = 32 h + r of an
+// operand holds row r: 4-bit elements of columns 32 h .. 32 h + 31 of the 64; 8-bit elements of columns
+// 16 h .. 16 h + 15 and 32 + 16 h .. 32 + 16 h + 15; in both cases the scale byte of block h.
 // (Found with an in-bounds check of the instruction's layout.)
 #include <algorithm>
 
-#include "mx.h"
+#include "mx_tile.h"
 
 namespace gptq {
 
 namespace {
 
-// Parts of an E4M3 operand whose exponents differ by at most 6: codes with the top exponent bit set, and the rest.
-// The matrix core aligns the products of one instruction to their largest and drops what lies more than about 13
-// bits below; with 7 exponents to each part nothing is dropped against E2M1 weights, so the sum is exact up to
-// fp32 rounding.
-__device__ __forceinline__ void split_e4m3(const i32x8& a, i32x8& hi, i32x8& lo) {
+struct MatmulArgs {
+  const uint8_t *ac, *as, *wc, *ws;
+  const float* bias;
+  void* Y;
+  int64_t n, ld;
+  int64_t crow_a, crow_w, srow;  // bytes of a row of codes and of scales
+  int out, ta, tb, grid;         // tiles along out and along tokens; workgroups of a slice
+  int nk, slice;                 // stages of 128 columns; stages of a slice
+  int relu, vec;
+};
+
+template <int FMT, bool SPLIT, bool YBF16, int WA, int WB, int MB, int NB, int NSTG, int OCC>
+__global__ __launch_bounds__(256, OCC) void k_mx_matmul(const MatmulArgs g) {
+  using T = TileProduct<K_E2M1, FMT == GPTQ_MX_E2M1 ? K_E2M1 : K_E4M3, WA, WB, MB, NB, NSTG, SPLIT>;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS];
+  int ia, ib;
+  if (!tile_of(blockIdx.x, g.grid, g.ta, g.tb, ia, ib)) return;
+  const int o0 = ia * WA;
+  const int64_t t0 = (int64_t)ib * WB;
+  const int ro = min(WA, g.out - o0);
+  const int rt = (int)min((int64_t)WB, g.n - t0);
+  const int k0 = blockIdx.y * g.slice, nk = min(g.slice, g.nk - k0);
+  T t;
+  t.init(lds);
+  constexpr int SB = FMT == GPTQ_MX_E2M1 ? 64 : 128;
+  t.a.mem.init(g.wc + (int64_t)o0 * g.crow_w + (int64_t)k0 * 64, ro * g.crow_w - (int64_t)k0 * 64, 64, nk);
+  t.b.mem.init(g.ac + t0 * g.crow_a + (int64_t)k0 * SB, rt * g.crow_a - (int64_t)k0 * SB, SB, nk);
+  t.sa.init(g.ws + (int64_t)o0 * g.srow + k0 * 4, ro * g.srow - k0 * 4, 16, (nk + 3) / 4);
+  t.sb.init(g.as + t0 * g.srow + k0 * 4, rt * g.srow - k0 * 4, 16, (nk + 3) / 4);
+  t.srow = g.srow;
+  t.a.init(g.crow_w, t.wave, t.lane, t.wa, 0);
+  t.b.init(g.crow_a, t.wave, t.lane, t.wb, 0);
+  t.run(nk);
+  const int64_t row0 = t0 + t.wb;
+  const int c0 = o0 + t.wa;
+  if (gridDim.y > 1) {
+    float* part = static_cast<float*>(g.Y) + blockIdx.y * g.n * (int64_t)g.out;
+    store_rows<false>(t.acc, lds, part, g.out, row0, g.n, c0, g.out, g.vec, false, [](int64_t, int, auto&) {});
+  } else {
+    store_rows<YBF16>(t.acc, lds, g.Y, g.ld, row0, g.n, c0, g.out, g.vec, false, [&](int64_t, int c, auto& v) {
+      constexpr int V = sizeof(v) / 4;
+      if (g.bias) {
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    const uint32_t t = (uint32_t)a[q] & 0x40404040u;
-    const uint32_t m = (t << 1) - (t >> 6);  // 0x7F in every byte whose top exponent bit is set
-    hi[q] = (int)((uint32_t)a[q] & m);
-    lo[q] = (int)((uint32_t)a[q] & ~m);
-    hi[q] |= (int)((uint32_t)a[q] & 0x80808080u);
+        for (int q = 0; q < V; ++q) v[q] += g.bias[min(c + q, g.out - 1)];
+      }
+      if (g.relu) {
+#pragma unroll
+        for (int q = 0; q < V; ++q) v[q] = relu_nan(v[q]);
+      }
+    });
   }
 }
 
-template <int FMT, bool SPLIT, bool YBF16>
-__global__ __launch_bounds__(256) void k_mx_matmul_simple(const uint8_t* __restrict__ ac, const uint8_t* __restrict__ as,
-                                                          int n, const uint8_t* __restrict__ wc,
-                                                          const uint8_t* __restrict__ wsc, int out, int kp, int64_t srow,
-                                                          const float* __restrict__ bias, int relu,
-                                                          void* __restrict__ Y, int64_t ld) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int r = lane & 31, h = lane >> 5;
-  const int tiles_o = (out + 63) / 64;
-  const int o0 = (blockIdx.x % tiles_o) * 64 + (wave & 1) * 32, t0 = (blockIdx.x / tiles_o) * 64 + (wave >> 1) * 32;
-  if (o0 >= out || t0 >= n) return;
-  const int o = min(o0 + r, out - 1), t = min(t0 + r, n - 1);  // rows past the end repeat the last; never stored
-  const uint8_t* wp = wc + (int64_t)o * (kp / 2);
-  const uint8_t* ap = ac + (int64_t)t * (FMT == GPTQ_MX_E2M1 ? kp / 2 : kp);
-  const uint8_t *wsp = wsc + o * srow, *asp = as + t * srow;
-  f32x16 acc;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-  for (int k = 0; k < kp; k += 64) {
-    i32x8 w = {0, 0, 0, 0, 0, 0, 0, 0}, a = {0, 0, 0, 0, 0, 0, 0, 0};
-    const uint4 wv = *reinterpret_cast<const uint4*>(wp + k / 2 + 16 * h);
-    w[0] = wv.x, w[1] = wv.y, w[2] = wv.z, w[3] = wv.w;
-    const int sw = wsp[k / 32 + h], sa = asp[k / 32 + h];
-    if (FMT == GPTQ_MX_E2M1) {
-      const uint4 v = *reinterpret_cast<const uint4*>(ap + k / 2 + 16 * h);
-      a[0] = v.x, a[1] = v.y, a[2] = v.z, a[3] = v.w;
-      acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, a, acc, 4, 4, 0, sw, 0, sa);
-    } else {
-      const uint4 v = *reinterpret_cast<const uint4*>(ap + k + 16 * h);
-      const uint4 u = *reinterpret_cast<const uint4*>(ap + k + 32 + 16 * h);
-      a[0] = v.x, a[1] = v.y, a[2] = v.z, a[3] = v.w, a[4] = u.x, a[5] = u.y, a[6] = u.z, a[7] = u.w;
-      if (SPLIT) {
-        i32x8 hi, lo;
-        split_e4m3(a, hi, lo);
-        acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, lo, acc, 4, 0, 0, sw, 0, sa);
-        acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, hi, acc, 4, 0, 0, sw, 0, sa);
-      } else {
-        acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, a, acc, 4, 0, 0, sw, 0, sa);
-      }
-    }
-  }
-  // result: register i of the lane holds column (of W's rows) 8 (i / 4) + 4 h + i % 4, token r
-  if (t0 + r >= n) return;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int c = o0 + 8 * (i >> 2) + 4 * h + (i & 3);
-    if (c >= out) continue;
-    float y = acc[i];
+// The slices' partial products, added in their order; bias, ReLU and the result's type.
+template <bool YBF16>
+__global__ __launch_bounds__(256) void k_mx_join(const float* __restrict__ part, int slices, int64_t n, int out,
+                                                 const float* __restrict__ bias, int relu, void* __restrict__ Y,
+                                                 int64_t ld) {
+  const int64_t total = n * out;
+  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += (int64_t)gridDim.x * 256) {
+    float y = 0.f;
+    for (int s = 0; s < slices; ++s) y += part[s * total + e];
+    const int64_t row = e / out;
+    const int c = (int)(e - row * out);
     if (bias) y += bias[c];
     if (relu) y = relu_nan(y);
-    const int64_t at = (int64_t)(t0 + r) * ld + c;
-    if (YBF16) static_cast<uint16_t*>(Y)[at] = (uint16_t)bf16_bits(y);
-    else static_cast<float*>(Y)[at] = y;
+    if (YBF16) static_cast<uint16_t*>(Y)[row * ld + c] = (uint16_t)bf16_bits(y);
+    else static_cast<float*>(Y)[row * ld + c] = y;
   }
+}
+
+struct MatmulPlan {
+  int tile;    // 0: 64 x 64, 1: 128 x 128, 2: 256 x 256
+  int slices;  // of k
+};
+
+MatmulPlan matmul_plan(int64_t n, int64_t in, int64_t out, int fmt) {
+  MatmulPlan p = {0, 1};
+  const int64_t nk = ceil_div(in, 128);
+  auto tiles = [&](int64_t w) { return ceil_div(n, w) * ceil_div(out, w); };
+  p.tile = tiles(256) >= 256 ? 2 : tiles(128) >= 256 ? 1 : 0;
+  (void)fmt;
+  if (p.tile == 0) {
+    const int64_t t = tiles(64);
+    if (t < 256) p.slices = (int)std::max<int64_t>(1, std::min<int64_t>({512 / t, ceil_div(nk, 8), 16}));
+  }
+  return p;
+}
+
+template <int FMT, bool SPLIT, bool YBF16>
+void matmul_go(int tile, dim3 grid, hipStream_t stream, const MatmulArgs& g) {
+  constexpr int LG = FMT == GPTQ_MX_E2M1 ? 4 : 3;
+  if (tile == 2) hipLaunchKernelGGL((k_mx_matmul<FMT, SPLIT, YBF16, 256, 256, 4, 4, LG, 1>), grid, dim3(256), 0, stream, g);
+  else if (tile == 1) hipLaunchKernelGGL((k_mx_matmul<FMT, SPLIT, YBF16, 128, 128, 2, 2, LG, 2>), grid, dim3(256), 0, stream, g);
+  else hipLaunchKernelGGL((k_mx_matmul<FMT, SPLIT, YBF16, 64, 64, 1, 1, 4, 3>), grid, dim3(256), 0, stream, g);
 }
 
 }  // namespace
 
-size_t mx_matmul_ws_bytes(int64_t, int64_t, int64_t, int) { return 0; }
+size_t mx_matmul_ws_bytes(int64_t n, int64_t in, int64_t out, int a_fmt) {
+  if (n == 0) return 0;
+  const MatmulPlan p = matmul_plan(n, in, out, a_fmt);
+  return p.slices > 1 ? align_up((size_t)p.slices * n * out * 4, 256) : 0;
+}
 
 hipError_t mx_matmul_launch(const MxMatrix& a, const MxMatrix& w, const float* bias, int relu, void* Y, int y_dtype,
-                            int64_t ld_y, void*, hipStream_t stream) {
-  const int kp = (int)ceil_div(a.cols, 128) * 128;
-  const int64_t tiles_o = ceil_div(w.rows, 64), srow = mx_scale_row(a.cols);
-  // at most 2^23 workgroups of 256 a launch
-  const int64_t rows_max = std::max<int64_t>(1, ((int64_t)1 << 23) / tiles_o) * 64;
+                            int64_t ld_y, void* ws, hipStream_t stream) {
+  const MatmulPlan p = matmul_plan(a.rows, a.cols, w.rows, a.fmt);
+  const bool bf16 = y_dtype == GPTQ_BF16;
+  const int64_t wt = 64 << p.tile, srow = mx_scale_row(a.cols), crow = mx_code_row(a.cols, a.fmt);
+  MatmulArgs g = {};
+  g.wc = w.codes, g.ws = w.scales, g.crow_a = crow, g.crow_w = mx_code_row(a.cols, GPTQ_MX_E2M1), g.srow = srow;
+  g.out = (int)w.rows, g.ta = (int)ceil_div(w.rows, wt), g.nk = (int)ceil_div(a.cols, 128);
+  g.slice = p.slices > 1 ? (int)ceil_div(ceil_div(g.nk, p.slices), 4) * 4 : g.nk;
+  const int slices = (int)ceil_div(g.nk, g.slice);
+  // at most 2^20 tiles a launch
+  const int64_t rows_max = p.slices > 1 ? a.rows : std::max<int64_t>(1, ((int64_t)1 << 20) / g.ta) * wt;
   for (int64_t r = 0; r < a.rows; r += rows_max) {
-    const int64_t n = std::min(rows_max, a.rows - r);
-    const dim3 grid((unsigned)(tiles_o * ceil_div(n, 64)));
-    const uint8_t *ac = a.codes + r * mx_code_row(a.cols, a.fmt), *as = a.scales + r * srow;
-    void* y = static_cast<uint8_t*>(Y) + r * ld_y * (y_dtype == GPTQ_BF16 ? 2 : 4);
-#define GPTQ_GO(F, S, B)                                                                                              \
-  hipLaunchKernelGGL((k_mx_matmul_simple<F, S, B>), grid, dim3(256), 0, stream, ac, as, (int)n, w.codes, w.scales,    \
-                     (int)w.rows, kp, srow, bias, relu, y, ld_y)
+    g.n = std::min(rows_max, a.rows - r);
+    g.tb = (int)ceil_div(g.n, wt);
+    g.grid = (int)tile_grid((int64_t)g.ta * g.tb);
+    g.ac = a.codes + r * crow, g.as = a.scales + r * srow;
+    g.bias = bias, g.relu = relu, g.ld = ld_y;
+    g.Y = static_cast<uint8_t*>(Y) + r * ld_y * (bf16 ? 2 : 4);
+    g.vec = vec_rows(g.Y, ld_y, y_dtype);
+    if (slices > 1) g.Y = ws, g.vec = w.rows % 4 == 0;
+    const dim3 grid((unsigned)g.grid, (unsigned)slices);
     if (a.fmt == GPTQ_MX_E2M1) {
-      if (y_dtype == GPTQ_BF16) GPTQ_GO(GPTQ_MX_E2M1, false, true);
-      else GPTQ_GO(GPTQ_MX_E2M1, false, false);
+      bf16 ? matmul_go<GPTQ_MX_E2M1, false, true>(p.tile, grid, stream, g)
+           : matmul_go<GPTQ_MX_E2M1, false, false>(p.tile, grid, stream, g);
     } else {
-      if (y_dtype == GPTQ_BF16) GPTQ_GO(GPTQ_MX_E4M3, false, true);
-      else GPTQ_GO(GPTQ_MX_E4M3, true, false);
+      bf16 ? matmul_go<GPTQ_MX_E4M3, false, true>(p.tile, grid, stream, g)
+           : matmul_go<GPTQ_MX_E4M3, true, false>(p.tile, grid, stream, g);
     }
-#undef GPTQ_GO
+  }
+  if (slices > 1) {
+    const unsigned grid = (unsigned)std::min<int64_t>(2048, ceil_div(a.rows * w.rows, 256));
+    if (bf16)
+      hipLaunchKernelGGL((k_mx_join<true>), dim3(grid), dim3(256), 0, stream, static_cast<const float*>(ws), slices,
+                         a.rows, (int)w.rows, bias, relu, Y, ld_y);
+    else
+      hipLaunchKernelGGL((k_mx_join<false>), dim3(grid), dim3(256), 0, stream, static_cast<const float*>(ws), slices,
+                         a.rows, (int)w.rows, bias, relu, Y, ld_y);
   }
   return hipGetLastError();
 }

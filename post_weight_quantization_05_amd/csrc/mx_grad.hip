@@ -2,139 +2,300 @@
 // and dW = dY^T A with db = column sums of dY.
 //
 // The quantized operand's values (4 significant bits at most, times a power of two) are exact in bf16, so it is first
-// written out in bf16 and the products run on the bf16 matrix cores, exact and summed in fp32.
-//
-// Simple form: a wave forms 32 x 32 of the result, its lanes loading their own elements of each step of 16 of the
-// summed dimension. The quantized operand is the first one, so that a lane of the result holds four consecutive
-// columns.
+// written out in bf16 and the products run on the bf16 matrix cores, exact and summed in fp32. It is the first operand,
+// so that a lane of the result holds four consecutive columns.
 #include <algorithm>
 
-#include "mx.h"
+#include "mx_tile.h"
 
 namespace gptq {
 
 namespace {
 
-// out[s][f] = sum_k F[k][f] S(k, s): S(k, s) = S[s][k] (GRAD_INPUT) or S[k][s] (weight gradient)
-template <bool GRAD_INPUT, bool YBF16, int MASK>
-__global__ __launch_bounds__(256) void k_mx_grad_simple(const uint16_t* __restrict__ F, int64_t ldf, int nf,
-                                                        const uint16_t* __restrict__ S, int64_t lds, int ns, int nk,
-                                                        const uint8_t* __restrict__ mc, const uint8_t* __restrict__ ms,
-                                                        int accumulate, void* __restrict__ Y, int64_t ld) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int r = lane & 31, h = lane >> 5;
-  const int tiles_f = (nf + 63) / 64;
-  const int f0 = (blockIdx.x % tiles_f) * 64 + (wave & 1) * 32, s0 = (blockIdx.x / tiles_f) * 64 + (wave >> 1) * 32;
-  if (f0 >= nf || s0 >= ns) return;
-  const int f = min(f0 + r, nf - 1), s = min(s0 + r, ns - 1);
-  f32x16 acc;
+struct GradArgs {
+  const uint16_t *F, *S;       // first operand [k][f]; second [s][k] (dX) or [k][s] (dW)
+  int64_t ldf, lds;            // their rows' elements
+  int64_t nk, slice;           // k; k of a slice (a multiple of 32)
+  int64_t ns;                  // rows of the result
+  int nf, ta, tb, grid;        // its columns; tiles along both; workgroups of a slice
+  const uint8_t *mc, *ms;      // mask
+  int64_t mrow, msrow;
+  void* Y;
+  int64_t ld;
+  int accumulate, vec;
+};
+
+// 4 consecutive columns' masks: zero where the mask's value is not > 0 (c a multiple of 4, below the row's padding)
+template <int MASK, int V>
+__device__ __forceinline__ void apply_mask(const GradArgs& g, int64_t row, int c, float (&v)[V]) {
+  const uint32_t scale = g.ms[row * g.msrow + (c >> 5)];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-  for (int k = 0; k < nk; k += 16) {
-    bf16x8 a, b;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int kk = k + 8 * h + j;
-      const bool ok = kk < nk;
-      const uint16_t av = ok ? F[(int64_t)kk * ldf + f] : (uint16_t)0;
-      const uint16_t bv = ok ? (GRAD_INPUT ? S[(int64_t)s * lds + kk] : S[(int64_t)kk * lds + s]) : (uint16_t)0;
-      a[j] = __builtin_bit_cast(__bf16, av);
-      b[j] = __builtin_bit_cast(__bf16, bv);
-    }
-    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, acc, 0, 0, 0);
-  }
-  if (s0 + r >= ns) return;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int c = f0 + 8 * (i >> 2) + 4 * h + (i & 3);
-    if (c >= nf) continue;
-    float y = acc[i];
-    if (MASK != 0) {
-      const int kp = (nf + 127) / 128 * 128, srow = (nf + 511) / 512 * 16;
-      uint32_t code;
-      bool pos;
-      if (MASK == 1) {
-        code = mc[(int64_t)s * (kp / 2) + (c >> 1)] >> (4 * (c & 1)) & 15u;
-        pos = code >= 1u && code <= 7u;
-      } else {
-        code = mc[(int64_t)s * kp + c];
-        pos = code >= 1u && code <= 0x7Eu;
-      }
-      if (!pos || ms[(int64_t)s * srow + (c >> 5)] == 255) y = 0.f;
-    }
-    const int64_t at = (int64_t)s * ld + c;
-    if (YBF16) {
-      static_cast<uint16_t*>(Y)[at] = (uint16_t)bf16_bits(y);
+  for (int q = 0; q < V; ++q) {
+    uint32_t code;
+    bool pos;
+    if (MASK == 1) {
+      code = (uint32_t)*reinterpret_cast<const uint16_t*>(g.mc + row * g.mrow + ((c + (q & ~3)) >> 1)) >> (4 * (q & 3)) & 15u;
+      pos = code >= 1u && code <= 7u;
     } else {
-      float* p = static_cast<float*>(Y) + at;
-      *p = accumulate ? *p + y : y;
+      code = *reinterpret_cast<const uint32_t*>(g.mc + row * g.mrow + c + (q & ~3)) >> (8 * (q & 3)) & 255u;
+      pos = code >= 1u && code <= 0x7Eu;
+    }
+    if (!pos || scale == 255u) v[q] = 0.f;
+  }
+}
+
+template <bool GRAD_INPUT, bool YBF16, int MASK, int WA, int WB, int MB, int NB, int NSTG, int OCC>
+__global__ __launch_bounds__(256, OCC) void k_mx_grad(const GradArgs g) {
+  using T = TileProduct<K_BF16T, GRAD_INPUT ? K_BF16 : K_BF16T, WA, WB, MB, NB, NSTG, false>;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS];
+  int ia, ib;
+  if (!tile_of(blockIdx.x, g.grid, g.ta, g.tb, ia, ib)) return;
+  const int f0 = ia * WA;
+  const int64_t s0 = (int64_t)ib * WB;
+  const int64_t k0 = blockIdx.y * g.slice, nk = min(g.slice, g.nk - k0);
+  const int stages = (int)((nk + 31) / 32);
+  T t;
+  t.init(lds);
+  // bytes from a tile's first element to the end of its last row (rounded up to whole 16-byte chunks)
+  t.a.mem.init(g.F + k0 * g.ldf + f0, ((nk - 1) * g.ldf + ((g.nf + 7) / 8 * 8 - f0)) * 2, (int)(32 * g.ldf * 2), stages);
+  t.a.init(g.ldf * 2, t.wave, t.lane, t.wa, g.nf - f0);
+  if (GRAD_INPUT) {
+    const int64_t rows = min((int64_t)WB, g.ns - s0);
+    t.b.mem.init(g.S + s0 * g.lds + k0, ((rows - 1) * g.lds + (int64_t)stages * 32) * 2, 64, stages);
+    t.b.init(g.lds * 2, t.wave, t.lane, t.wb, 0);
+  } else {
+    t.b.mem.init(g.S + k0 * g.lds + s0, ((nk - 1) * g.lds + ((g.ns + 7) / 8 * 8 - s0)) * 2, (int)(32 * g.lds * 2), stages);
+    t.b.init(g.lds * 2, t.wave, t.lane, t.wb, g.ns - s0);
+  }
+  t.run(stages);
+  const int64_t row0 = s0 + t.wb;
+  const int c0 = f0 + t.wa;
+  if (gridDim.y > 1) {
+    float* part = static_cast<float*>(g.Y) + blockIdx.y * g.ns * (int64_t)g.nf;
+    store_rows<false>(t.acc, lds, part, g.nf, row0, g.ns, c0, g.nf, g.vec, false, [](int64_t, int, auto&) {});
+  } else {
+    store_rows<YBF16>(t.acc, lds, g.Y, g.ld, row0, g.ns, c0, g.nf, g.vec, g.accumulate, [&](int64_t row, int c, auto& v) {
+      if constexpr (MASK != 0) apply_mask<MASK>(g, row, c, v);
+    });
+  }
+}
+
+// The slices' partial products, added in their order; mask, accumulation and the result's type. Four columns a thread.
+template <bool YBF16, int MASK>
+__global__ __launch_bounds__(256) void k_mx_grad_join(const GradArgs g, const float* __restrict__ part, int slices) {
+  const int per_row = (g.nf + 3) / 4;
+  const int64_t total = g.ns * per_row, stride = g.ns * (int64_t)g.nf;
+  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += (int64_t)gridDim.x * 256) {
+    const int64_t row = e / per_row;
+    const int c = (int)(e - row * per_row) * 4;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < slices; ++s)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (c + q < g.nf) v[q] += part[s * stride + row * g.nf + c + q];
+    if constexpr (MASK != 0) apply_mask<MASK>(g, row, c, v);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (c + q >= g.nf) continue;
+      if (YBF16) {
+        static_cast<uint16_t*>(g.Y)[row * g.ld + c + q] = (uint16_t)bf16_bits(v[q]);
+      } else {
+        float* p = static_cast<float*>(g.Y) + row * g.ld + c + q;
+        *p = g.accumulate ? *p + v[q] : v[q];
+      }
     }
   }
 }
 
-__global__ __launch_bounds__(256) void k_colsum_simple(const uint16_t* __restrict__ S, int64_t ld, int64_t n, int cols,
-                                                       int accumulate, float* __restrict__ db) {
+// dY with rows of kp (a multiple of 32) columns, zeros behind the last
+__global__ __launch_bounds__(256) void k_pad_rows(const uint16_t* __restrict__ X, int64_t ld, int64_t n, int cols, int kp,
+                                                  uint16_t* __restrict__ Y) {
+  const int64_t total = n * (kp / 8);
+  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += (int64_t)gridDim.x * 256) {
+    const int64_t row = e / (kp / 8);
+    const int c = (int)(e - row * (kp / 8)) * 8;
+    const uint16_t* p = X + row * ld + c;
+    uint32_t w[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t lo = c + 2 * q < cols ? p[2 * q] : 0u, hi = c + 2 * q + 1 < cols ? p[2 * q + 1] : 0u;
+      w[q] = lo | hi << 16;
+    }
+    *reinterpret_cast<uint4*>(Y + row * kp + c) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// Column sums of dY in fp64: workgroup (x, y) adds 32 columns of a slice of rows, eight row groups side by side; the
+// slices are then added in their order.
+constexpr int SUM_ROWS = 256;
+__global__ __launch_bounds__(256) void k_colsum(const uint16_t* __restrict__ S, int64_t ld, int64_t n, int cols,
+                                                int64_t rows, double* __restrict__ part) {
+  __shared__ double red[8][32];
+  const int c = blockIdx.x * 32 + (threadIdx.x & 31), g = threadIdx.x >> 5;
+  const int64_t r0 = blockIdx.y * rows, r1 = min(n, r0 + rows);
+  double sum = 0.0;
+  if (c < cols)
+#pragma unroll 4
+    for (int64_t k = r0 + g; k < r1; k += 8) sum += (double)__uint_as_float((uint32_t)S[k * ld + c] << 16);
+  red[g][threadIdx.x & 31] = sum;
+  __syncthreads();
+  if (g == 0 && c < cols) {
+#pragma unroll
+    for (int q = 1; q < 8; ++q) sum += red[q][threadIdx.x];
+    part[(int64_t)blockIdx.y * cols + c] = sum;
+  }
+}
+__global__ __launch_bounds__(256) void k_colsum_join(const double* __restrict__ part, int slices, int cols,
+                                                     int accumulate, float* __restrict__ db) {
   const int c = blockIdx.x * 256 + threadIdx.x;
   if (c >= cols) return;
-  double sum = 0.0;
-  for (int64_t k = 0; k < n; ++k) sum += (double)__uint_as_float((uint32_t)S[k * ld + c] << 16);
-  db[c] = (float)(accumulate ? (double)db[c] + sum : sum);
+  double sum = accumulate ? (double)db[c] : 0.0;
+  for (int s = 0; s < slices; ++s) sum += part[(int64_t)s * cols + c];
+  db[c] = (float)sum;
 }
+
+struct GradPlan {
+  int tile;    // 0: 64 x 64, 1: 128 x 128, 2: 256 x 256
+  int slices;
+  int64_t slice;
+};
+
+GradPlan grad_plan(int64_t ns, int64_t nf, int64_t nk) {
+  GradPlan p = {0, 1, std::max<int64_t>(32, (int64_t)align_up(nk, 32))};
+  auto tiles = [&](int64_t w) { return ceil_div(ns, w) * ceil_div(nf, w); };
+  p.tile = tiles(256) >= 192 ? 2 : tiles(128) >= 192 ? 1 : 0;
+  const int64_t t = tiles(64 << p.tile);
+  if (t > 0 && t < 192) {
+    const int64_t s = std::max<int64_t>(1, std::min<int64_t>({512 / t, ceil_div(nk, 256), 64}));
+    p.slice = std::max<int64_t>(32, (int64_t)align_up(ceil_div(nk, s), 32));
+  }
+  p.slices = (int)std::max<int64_t>(1, ceil_div(nk, p.slice));
+  return p;
+}
+
+size_t grad_part_bytes(const GradPlan& p, int64_t ns, int64_t nf) {
+  return p.slices > 1 ? align_up((size_t)p.slices * ns * nf * 4, 256) : 0;
+}
+
+template <bool GI, bool B, int M>
+void grad_go(int tile, dim3 grid, hipStream_t stream, const GradArgs& g) {
+  if (tile == 2) hipLaunchKernelGGL((k_mx_grad<GI, B, M, 256, 256, 4, 4, 4, 1>), grid, dim3(256), 0, stream, g);
+  else if (tile == 1) hipLaunchKernelGGL((k_mx_grad<GI, B, M, 128, 128, 2, 2, 5, 2>), grid, dim3(256), 0, stream, g);
+  else hipLaunchKernelGGL((k_mx_grad<GI, B, M, 64, 64, 1, 1, 5, 3>), grid, dim3(256), 0, stream, g);
+}
+
+template <bool GI, bool B, int M>
+hipError_t grad_run(const GradPlan& p, GradArgs g, float* part, hipStream_t stream) {
+  const GradArgs fin = g;
+  g.slice = p.slice;
+  g.ta = (int)ceil_div(g.nf, 64 << p.tile);
+  if (p.slices > 1) g.Y = part, g.ld = g.nf, g.vec = g.nf % 4 == 0;
+  g.tb = (int)ceil_div(g.ns, 64 << p.tile);
+  g.grid = (int)tile_grid((int64_t)g.ta * g.tb);
+  grad_go<GI, B, M>(p.tile, dim3((unsigned)g.grid, (unsigned)p.slices), stream, g);
+  if (p.slices > 1)
+    hipLaunchKernelGGL((k_mx_grad_join<B, M>), dim3((unsigned)std::min<int64_t>(2048, ceil_div(g.ns * ceil_div(g.nf, 4), 256))),
+                       dim3(256), 0, stream, fin, part, p.slices);
+  return hipGetLastError();
+}
+
+// The tile product reads dY with 16-byte loads of whole chunks; where rows are not aligned, or a row's tail would
+// bring its neighbour's numbers into the sum (dX), a padded copy is read instead.
+bool dy_direct(const uint16_t* dY, int64_t ld, int64_t out, bool sum_over_out) {
+  return vec_rows(dY, ld, GPTQ_BF16) && ld <= ((int64_t)1 << 20) && (!sum_over_out || out % 32 == 0);
+}
+
+constexpr int64_t ROWS_MAX = (int64_t)1 << 20;  // rows of dX a launch
 
 }  // namespace
 
-size_t mx_grad_input_ws_bytes(int64_t, int64_t in, int64_t out) { return align_up(out * ceil_div(in, 128) * 256, 256); }
-size_t mx_grad_weight_ws_bytes(int64_t n, int64_t in, int64_t) { return align_up(n * ceil_div(in, 128) * 256, 256); }
+size_t mx_grad_input_ws_bytes(int64_t n, int64_t in, int64_t out) {
+  const int64_t m = std::min(n, ROWS_MAX);
+  return align_up(out * ceil_div(in, 128) * 256, 256) + align_up(m * ceil_div(out, 128) * 256, 256) +
+         grad_part_bytes(grad_plan(m, in, out), m, in);
+}
 
 hipError_t mx_grad_input_launch(const uint16_t* dY, int64_t ld_dy, int64_t n, const MxMatrix& w, const MxMatrix* mask,
                                 void* dX, int dx_dtype, int64_t ld_dx, void* ws, hipStream_t stream) {
-  const int64_t in = w.cols, ldf = ceil_div(in, 128) * 128;
+  const int64_t in = w.cols, out = w.rows, ldf = ceil_div(in, 128) * 128, kp = ceil_div(out, 128) * 128;
   const hipError_t e = mx_dequantize_launch(w, ws, GPTQ_BF16, ldf, stream);
   if (e != hipSuccess) return e;
-  const uint16_t* F = static_cast<const uint16_t*>(ws);
-  const int64_t tiles_f = ceil_div(in, 64), rows_max = std::max<int64_t>(1, ((int64_t)1 << 23) / tiles_f) * 64;
-  for (int64_t r = 0; r < n; r += rows_max) {
-    const int64_t m = std::min(rows_max, n - r);
-    const dim3 grid((unsigned)(tiles_f * ceil_div(m, 64)));
-    const uint8_t* mc = mask ? mask->codes + r * mx_code_row(in, mask->fmt) : nullptr;
-    const uint8_t* ms = mask ? mask->scales + r * mx_scale_row(in) : nullptr;
-    void* y = static_cast<uint8_t*>(dX) + r * ld_dx * (dx_dtype == GPTQ_BF16 ? 2 : 4);
-    const int kind = !mask ? 0 : mask->fmt == GPTQ_MX_E2M1 ? 1 : 2;
-#define GPTQ_GO(B, M)                                                                                                \
-  hipLaunchKernelGGL((k_mx_grad_simple<true, B, M>), grid, dim3(256), 0, stream, F, ldf, (int)in, dY + r * ld_dy,    \
-                     ld_dy, (int)m, (int)w.rows, mc, ms, 0, y, ld_dx)
-    if (dx_dtype == GPTQ_BF16) {
-      if (kind == 0) GPTQ_GO(true, 0);
-      else if (kind == 1) GPTQ_GO(true, 1);
-      else GPTQ_GO(true, 2);
-    } else {
-      if (kind == 0) GPTQ_GO(false, 0);
-      else if (kind == 1) GPTQ_GO(false, 1);
-      else GPTQ_GO(false, 2);
+  uint8_t* pad = static_cast<uint8_t*>(ws) + align_up(out * ldf * 2, 256);
+  float* part = reinterpret_cast<float*>(pad + align_up(std::min(n, ROWS_MAX) * kp * 2, 256));
+  for (int64_t r = 0; r < n; r += ROWS_MAX) {
+    GradArgs g = {};
+    g.F = static_cast<const uint16_t*>(ws), g.ldf = ldf, g.nk = out;
+    g.S = dY + r * ld_dy, g.lds = ld_dy, g.ns = std::min(ROWS_MAX, n - r), g.nf = (int)in;
+    if (!dy_direct(g.S, ld_dy, out, true)) {
+      hipLaunchKernelGGL(k_pad_rows, dim3((unsigned)std::min<int64_t>(4096, ceil_div(g.ns * (kp / 8), 256))), dim3(256), 0,
+                         stream, g.S, ld_dy, g.ns, (int)out, (int)kp, reinterpret_cast<uint16_t*>(pad));
+      g.S = reinterpret_cast<const uint16_t*>(pad), g.lds = kp;
     }
-#undef GPTQ_GO
+    if (mask) {
+      g.mrow = mx_code_row(in, mask->fmt), g.msrow = mx_scale_row(in);
+      g.mc = mask->codes + r * g.mrow, g.ms = mask->scales + r * g.msrow;
+    }
+    g.Y = static_cast<uint8_t*>(dX) + r * ld_dx * (dx_dtype == GPTQ_BF16 ? 2 : 4), g.ld = ld_dx;
+    g.vec = vec_rows(g.Y, ld_dx, dx_dtype);
+    // the plan of the first (largest) piece: its partial products fit the workspace
+    const GradPlan p = grad_plan(std::min(n, ROWS_MAX), in, out);
+    const int kind = !mask ? 0 : mask->fmt == GPTQ_MX_E2M1 ? 1 : 2;
+    hipError_t s;
+    if (dx_dtype == GPTQ_BF16)
+      s = kind == 0 ? grad_run<true, true, 0>(p, g, part, stream)
+                    : kind == 1 ? grad_run<true, true, 1>(p, g, part, stream) : grad_run<true, true, 2>(p, g, part, stream);
+    else
+      s = kind == 0 ? grad_run<true, false, 0>(p, g, part, stream)
+                    : kind == 1 ? grad_run<true, false, 1>(p, g, part, stream) : grad_run<true, false, 2>(p, g, part, stream);
+    if (s != hipSuccess) return s;
   }
-  return hipGetLastError();
+  return hipSuccess;
+}
+
+namespace {
+int64_t colsum_rows(int64_t n, int64_t out) {
+  const int64_t want = std::max<int64_t>(1, 2048 / ceil_div(out, 32));  // about 2048 workgroups
+  return std::max<int64_t>(SUM_ROWS, ceil_div(n, std::min<int64_t>(want, 1024)));
+}
+}  // namespace
+
+size_t mx_grad_weight_ws_bytes(int64_t n, int64_t in, int64_t out) {
+  return align_up(n * ceil_div(in, 128) * 256, 256) + align_up(n * ceil_div(out, 128) * 256, 256) +
+         grad_part_bytes(grad_plan(out, in, n), out, in) + align_up(ceil_div(n, colsum_rows(n, out)) * out * 8, 256);
 }
 
 hipError_t mx_grad_weight_launch(const uint16_t* dY, int64_t ld_dy, int64_t out, const MxMatrix& a, int accumulate,
                                  void* dW, int dw_dtype, int64_t ld_dw, float* db, void* ws, hipStream_t stream) {
-  const int64_t in = a.cols, ldf = ceil_div(in, 128) * 128;
-  if (a.rows > 0) {
+  const int64_t n = a.rows, in = a.cols, ldf = ceil_div(in, 128) * 128, kp = ceil_div(out, 128) * 128;
+  uint8_t* pad = static_cast<uint8_t*>(ws) + align_up(n * ldf * 2, 256);
+  uint8_t* part = pad + align_up(n * kp * 2, 256);
+  const GradPlan p = grad_plan(out, in, n);
+  double* sums = reinterpret_cast<double*>(part + grad_part_bytes(p, out, in));
+  GradArgs g = {};
+  g.F = static_cast<const uint16_t*>(ws), g.ldf = ldf, g.nk = n, g.nf = (int)in;
+  g.S = dY, g.lds = ld_dy, g.ns = out, g.Y = dW, g.ld = ld_dw, g.accumulate = accumulate;
+  g.vec = vec_rows(dW, ld_dw, dw_dtype);
+  if (n > 0) {
     const hipError_t e = mx_dequantize_launch(a, ws, GPTQ_BF16, ldf, stream);
     if (e != hipSuccess) return e;
+    if (!dy_direct(dY, ld_dy, out, false)) {
+      hipLaunchKernelGGL(k_pad_rows, dim3((unsigned)std::min<int64_t>(4096, ceil_div(n * (kp / 8), 256))), dim3(256), 0,
+                         stream, dY, ld_dy, n, (int)out, (int)kp, reinterpret_cast<uint16_t*>(pad));
+      g.S = reinterpret_cast<const uint16_t*>(pad), g.lds = kp;
+    }
   }
-  const uint16_t* F = static_cast<const uint16_t*>(ws);
-  const dim3 grid((unsigned)(ceil_div(in, 64) * ceil_div(out, 64)));
-  if (dw_dtype == GPTQ_BF16)
-    hipLaunchKernelGGL((k_mx_grad_simple<false, true, 0>), grid, dim3(256), 0, stream, F, ldf, (int)in, dY, ld_dy,
-                       (int)out, (int)a.rows, nullptr, nullptr, 0, dW, ld_dw);
-  else
-    hipLaunchKernelGGL((k_mx_grad_simple<false, false, 0>), grid, dim3(256), 0, stream, F, ldf, (int)in, dY, ld_dy,
-                       (int)out, (int)a.rows, nullptr, nullptr, accumulate, dW, ld_dw);
-  if (db)
-    hipLaunchKernelGGL(k_colsum_simple, dim3((unsigned)ceil_div(out, 256)), dim3(256), 0, stream, dY, ld_dy, a.rows,
-                       (int)out, accumulate, db);
+  const hipError_t s = dw_dtype == GPTQ_BF16 ? grad_run<false, true, 0>(p, g, reinterpret_cast<float*>(part), stream)
+                                             : grad_run<false, false, 0>(p, g, reinterpret_cast<float*>(part), stream);
+  if (s != hipSuccess) return s;
+  if (db) {
+    const int64_t rows = colsum_rows(n, out);
+    const int slices = (int)ceil_div(n, rows);
+    if (slices)
+      hipLaunchKernelGGL(k_colsum, dim3((unsigned)ceil_div(out, 32), (unsigned)slices), dim3(256), 0, stream, dY, ld_dy, n,
+                         (int)out, rows, sums);
+    hipLaunchKernelGGL(k_colsum_join, dim3((unsigned)ceil_div(out, 256)), dim3(256), 0, stream, sums, slices, (int)out,
+                       accumulate, db);
+  }
   return hipGetLastError();
 }
 

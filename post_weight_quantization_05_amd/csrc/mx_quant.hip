@@ -197,10 +197,6 @@ __global__ __launch_bounds__(256) void k_mx_dequantize(const uint8_t* __restrict
   }
 }
 
-bool vec_rows(const void* p, int64_t ld, int dtype) {
-  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * (dtype == GPTQ_F32 ? 4 : 2)) % 16 == 0;
-}
-
 template <int FMT, bool B>
 void quantize_go(bool vec, unsigned grid, hipStream_t stream, const void* X, int64_t ld, int in, int ks, int64_t units,
                  uint8_t* codes, uint8_t* scales) {
