@@ -20,51 +20,83 @@ struct MatmulArgs {
   void* Y;
   int64_t n, ld;
   int64_t crow_a, crow_w, srow;  // bytes of a row of codes and of scales
-  int out, ta, tb, grid;         // tiles along out and along tokens; workgroups of a slice
-  int nk, slice;                 // stages of 128 columns; stages of a slice
+  int out, ta, tb;               // tiles along out and along tokens
+  int nk, slice;                 // 128s of columns; those of a slice (a multiple of 4)
   int relu, vec;
 };
 
-template <int FMT, bool SPLIT, bool YBF16, int WA, int WB, int MB, int NB, int NSTG, int OCC>
-__global__ __launch_bounds__(256, OCC) void k_mx_matmul(const MatmulArgs g) {
-  using T = TileProduct<K_E2M1, FMT == GPTQ_MX_E2M1 ? K_E2M1 : K_E4M3, WA, WB, MB, NB, NSTG, SPLIT>;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS];
-  int ia, ib;
-  if (!tile_of(blockIdx.x, g.grid, g.ta, g.tb, ia, ib)) return;
-  const int o0 = ia * WA;
-  const int64_t t0 = (int64_t)ib * WB;
-  const int ro = min(WA, g.out - o0);
-  const int rt = (int)min((int64_t)WB, g.n - t0);
-  const int k0 = blockIdx.y * g.slice, nk = min(g.slice, g.nk - k0);
-  T t;
-  t.init(lds);
-  constexpr int SB = FMT == GPTQ_MX_E2M1 ? 64 : 128;
-  t.a.mem.init(g.wc + (int64_t)o0 * g.crow_w + (int64_t)k0 * 64, ro * g.crow_w - (int64_t)k0 * 64, 64, nk);
-  t.b.mem.init(g.ac + t0 * g.crow_a + (int64_t)k0 * SB, rt * g.crow_a - (int64_t)k0 * SB, SB, nk);
-  t.sa.init(g.ws + (int64_t)o0 * g.srow + k0 * 4, ro * g.srow - k0 * 4, 16, (nk + 3) / 4);
-  t.sb.init(g.as + t0 * g.srow + k0 * 4, rt * g.srow - k0 * 4, 16, (nk + 3) / 4);
-  t.srow = g.srow;
-  t.a.init(g.crow_w, t.wave, t.lane, t.wa, 0);
-  t.b.init(g.crow_a, t.wave, t.lane, t.wb, 0);
-  t.run(nk);
-  const int64_t row0 = t0 + t.wb;
-  const int c0 = o0 + t.wa;
-  if (gridDim.y > 1) {
-    float* part = static_cast<float*>(g.Y) + blockIdx.y * g.n * (int64_t)g.out;
-    store_rows<false>(t.acc, lds, part, g.out, row0, g.n, c0, g.out, g.vec, false, [](int64_t, int, auto&) {});
-  } else {
-    store_rows<YBF16>(t.acc, lds, g.Y, g.ld, row0, g.n, c0, g.out, g.vec, false, [&](int64_t, int c, auto& v) {
-      constexpr int V = sizeof(v) / 4;
-      if (g.bias) {
+// bias (may be null) and ReLU
+template <int V>
+struct StoreLinear {
+  const float* bias;
+  float low, b[V];
+  __device__ __forceinline__ float relu(float v) { return v < low ? low : v; }  // NaN stays
+  __device__ __forceinline__ void columns(int c) {
 #pragma unroll
-        for (int q = 0; q < V; ++q) v[q] += g.bias[min(c + q, g.out - 1)];
-      }
-      if (g.relu) {
+    for (int q = 0; q < V; ++q) b[q] = 0.f;
+    if (bias) {
 #pragma unroll
-        for (int q = 0; q < V; ++q) v[q] = relu_nan(v[q]);
-      }
-    });
+      for (int q = 0; q < V; ++q) b[q] = bias[c + q];
+    }
   }
+  __device__ __forceinline__ void row(int, int, int64_t, int) {}
+  __device__ __forceinline__ void settle(int) {}
+  __device__ __forceinline__ void finish(int, int, float (&v)[V]) {
+#pragma unroll
+    for (int q = 0; q < V; ++q) v[q] = relu(v[q] + b[q]);
+  }
+  __device__ __forceinline__ float one(int64_t, int c, float v) { return relu(bias ? v + bias[c] : v); }
+};
+
+template <int FMT, bool SPLIT, bool YBF16, int WA, int WB, int MB, int NB, int OCC>
+__global__ __launch_bounds__(256, OCC) void k_mx_matmul(const MatmulArgs g) {
+  using T = TileProduct<K_E2M1, FMT == GPTQ_MX_E2M1 ? K_E2M1 : K_E4M3, WA, WB, MB, NB, SPLIT>;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS];
+  TileOrder order;
+  order.init(blockIdx.x, gridDim.x, g.ta, g.tb);
+  int ia, ib;
+  if (!order.get(0, ia, ib)) return;
+  const int k0 = blockIdx.y * g.slice, nk = min(g.slice, g.nk - k0);
+  const int stages = (nk + 1) / 2;
+  const int64_t wk = (int64_t)k0 * 64, ak = (int64_t)k0 * (FMT == GPTQ_MX_E2M1 ? 64 : 128);
+  T t;
+  t.init(lds, g.srow);
+  t.a.init(g.crow_w, t.wave, t.lane, t.wa);
+  t.b.init(g.crow_a, t.wave, t.lane, t.wb);
+  t.tail = __builtin_amdgcn_readfirstlane(nk & 1);
+  auto locate = [&](bool any, Stretch& a, Stretch& b, Stretch& sa, Stretch& sb) {
+    const int o0 = ia * WA;
+    const int64_t t0 = (int64_t)ib * WB;
+    const int ro = min(WA, g.out - o0), rt = (int)min((int64_t)WB, g.n - t0);
+    const int n = any ? stages : 0;
+    a.init(g.wc + (int64_t)o0 * g.crow_w + wk, ro * g.crow_w - wk, T::A::STEP, n);
+    b.init(g.ac + t0 * g.crow_a + ak, rt * g.crow_a - ak, T::B::STEP, n);
+    sa.init(g.ws + (int64_t)o0 * g.srow + k0 * 4, ro * g.srow - k0 * 4, 32, n);
+    sb.init(g.as + t0 * g.srow + k0 * 4, rt * g.srow - k0 * 4, 32, n);
+  };
+  locate(true, t.a.mem, t.b.mem, t.sa, t.sb);
+  t.start();
+  bool more = true;
+  for (int r = 1; more; ++r) {
+    const int64_t row0 = (int64_t)ib * WB + t.wb;
+    const int c0 = ia * WA + t.wa;
+    more = order.get(r, ia, ib);
+    locate(more, t.an, t.bn, t.san, t.sbn);
+    t.multiply((stages + 1) / 2 * 2);
+    if (!T::STAYS) wait_and_barrier<0>();
+    uint8_t* buf = T::STAYS ? lds + T::LDS - 4 * 4096 * T::PB : lds;
+    if (gridDim.y > 1) {
+      float* part = static_cast<float*>(g.Y) + blockIdx.y * g.n * (int64_t)g.out;
+      store_rows<false, T::PB>(t.acc, buf, part, g.ld, row0, g.n, c0, g.out, g.vec, false, StoreAsIs());
+    } else {
+      StoreLinear<YBF16 ? 8 : 4> done;
+      done.bias = g.bias, done.low = g.relu ? 0.f : -__builtin_inff();
+      store_rows<YBF16, T::PB>(t.acc, buf, g.Y, g.ld, row0, g.n, c0, g.out, g.vec, false, done);
+    }
+    if (!T::STAYS) return;
+    t.clear();
+  }
+  wait_and_barrier<0>();  // nothing may still be writing LDS when the workgroup ends
 }
 
 // The slices' partial products, added in their order; bias, ReLU and the result's type.
@@ -85,30 +117,43 @@ __global__ __launch_bounds__(256) void k_mx_join(const float* __restrict__ part,
   }
 }
 
+// Tile sizes along out and along tokens. A stage of E4M3 tokens is twice that of E2M1 ones, so its large tile has half
+// the tokens.
 struct MatmulPlan {
-  int tile;    // 0: 64 x 64, 1: 128 x 128, 2: 256 x 256
+  int wa, wb;
   int slices;  // of k
 };
 
 MatmulPlan matmul_plan(int64_t n, int64_t in, int64_t out, int fmt) {
-  MatmulPlan p = {0, 1};
   const int64_t nk = ceil_div(in, 128);
-  auto tiles = [&](int64_t w) { return ceil_div(n, w) * ceil_div(out, w); };
-  p.tile = tiles(256) >= 256 ? 2 : tiles(128) >= 256 ? 1 : 0;
-  (void)fmt;
-  if (p.tile == 0) {
-    const int64_t t = tiles(64);
-    if (t < 256) p.slices = (int)std::max<int64_t>(1, std::min<int64_t>({512 / t, ceil_div(nk, 8), 16}));
+  auto tiles = [&](int64_t a, int64_t b) { return ceil_div(out, a) * ceil_div(n, b); };
+  MatmulPlan p = {64, 64, 1};
+  if (fmt == GPTQ_MX_E2M1) {
+    if (tiles(256, 256) >= 256) p = {256, 256, 1};
+    else if (tiles(128, 128) >= 256) p = {128, 128, 1};
+  } else {
+    if (tiles(256, 128) >= 256) p = {256, 128, 1};
+    else if (tiles(128, 64) >= 256) p = {128, 64, 1};
   }
+  const int64_t t = tiles(p.wa, p.wb);
+  if (t > 0 && t < 256) p.slices = (int)std::max<int64_t>(1, std::min<int64_t>({512 / t, ceil_div(nk, 8), 16}));
   return p;
 }
 
 template <int FMT, bool SPLIT, bool YBF16>
-void matmul_go(int tile, dim3 grid, hipStream_t stream, const MatmulArgs& g) {
-  constexpr int LG = FMT == GPTQ_MX_E2M1 ? 4 : 3;
-  if (tile == 2) hipLaunchKernelGGL((k_mx_matmul<FMT, SPLIT, YBF16, 256, 256, 4, 4, LG, 1>), grid, dim3(256), 0, stream, g);
-  else if (tile == 1) hipLaunchKernelGGL((k_mx_matmul<FMT, SPLIT, YBF16, 128, 128, 2, 2, LG, 2>), grid, dim3(256), 0, stream, g);
-  else hipLaunchKernelGGL((k_mx_matmul<FMT, SPLIT, YBF16, 64, 64, 1, 1, 4, 3>), grid, dim3(256), 0, stream, g);
+void matmul_go(const MatmulPlan& p, dim3 grid, hipStream_t stream, const MatmulArgs& g) {
+#define GPTQ_GO(WA, WB, MB, NB, OCC) \
+  hipLaunchKernelGGL((k_mx_matmul<FMT, SPLIT, YBF16, WA, WB, MB, NB, OCC>), grid, dim3(256), 0, stream, g)
+  if (p.wa == 64) {
+    GPTQ_GO(64, 64, 1, 1, 2);
+  } else if constexpr (FMT == GPTQ_MX_E2M1) {
+    if (p.wa == 256) GPTQ_GO(256, 256, 4, 4, 1);
+    else GPTQ_GO(128, 128, 2, 2, 2);
+  } else {
+    if (p.wa == 256) GPTQ_GO(256, 128, 4, 2, 1);
+    else GPTQ_GO(128, 64, 2, 1, 2);
+  }
+#undef GPTQ_GO
 }
 
 }  // namespace
@@ -123,30 +168,29 @@ hipError_t mx_matmul_launch(const MxMatrix& a, const MxMatrix& w, const float* b
                             int64_t ld_y, void* ws, hipStream_t stream) {
   const MatmulPlan p = matmul_plan(a.rows, a.cols, w.rows, a.fmt);
   const bool bf16 = y_dtype == GPTQ_BF16;
-  const int64_t wt = 64 << p.tile, srow = mx_scale_row(a.cols), crow = mx_code_row(a.cols, a.fmt);
+  const int64_t srow = mx_scale_row(a.cols), crow = mx_code_row(a.cols, a.fmt);
   MatmulArgs g = {};
   g.wc = w.codes, g.ws = w.scales, g.crow_a = crow, g.crow_w = mx_code_row(a.cols, GPTQ_MX_E2M1), g.srow = srow;
-  g.out = (int)w.rows, g.ta = (int)ceil_div(w.rows, wt), g.nk = (int)ceil_div(a.cols, 128);
+  g.out = (int)w.rows, g.ta = (int)ceil_div(w.rows, p.wa), g.nk = (int)ceil_div(a.cols, 128);
   g.slice = p.slices > 1 ? (int)ceil_div(ceil_div(g.nk, p.slices), 4) * 4 : g.nk;
   const int slices = (int)ceil_div(g.nk, g.slice);
   // at most 2^20 tiles a launch
-  const int64_t rows_max = p.slices > 1 ? a.rows : std::max<int64_t>(1, ((int64_t)1 << 20) / g.ta) * wt;
+  const int64_t rows_max = p.slices > 1 ? a.rows : std::max<int64_t>(1, ((int64_t)1 << 20) / g.ta) * p.wb;
   for (int64_t r = 0; r < a.rows; r += rows_max) {
     g.n = std::min(rows_max, a.rows - r);
-    g.tb = (int)ceil_div(g.n, wt);
-    g.grid = (int)tile_grid((int64_t)g.ta * g.tb);
+    g.tb = (int)ceil_div(g.n, p.wb);
     g.ac = a.codes + r * crow, g.as = a.scales + r * srow;
     g.bias = bias, g.relu = relu, g.ld = ld_y;
     g.Y = static_cast<uint8_t*>(Y) + r * ld_y * (bf16 ? 2 : 4);
     g.vec = vec_rows(g.Y, ld_y, y_dtype);
-    if (slices > 1) g.Y = ws, g.vec = w.rows % 4 == 0;
-    const dim3 grid((unsigned)g.grid, (unsigned)slices);
+    if (slices > 1) g.Y = ws, g.ld = w.rows, g.vec = w.rows % 4 == 0;
+    const dim3 grid(tile_grid((int64_t)g.ta * g.tb, p.wa == 256 ? 256 : 1 << 30), (unsigned)slices);
     if (a.fmt == GPTQ_MX_E2M1) {
-      bf16 ? matmul_go<GPTQ_MX_E2M1, false, true>(p.tile, grid, stream, g)
-           : matmul_go<GPTQ_MX_E2M1, false, false>(p.tile, grid, stream, g);
+      bf16 ? matmul_go<GPTQ_MX_E2M1, false, true>(p, grid, stream, g)
+           : matmul_go<GPTQ_MX_E2M1, false, false>(p, grid, stream, g);
     } else {
-      bf16 ? matmul_go<GPTQ_MX_E4M3, false, true>(p.tile, grid, stream, g)
-           : matmul_go<GPTQ_MX_E4M3, true, false>(p.tile, grid, stream, g);
+      bf16 ? matmul_go<GPTQ_MX_E4M3, false, true>(p, grid, stream, g)
+           : matmul_go<GPTQ_MX_E4M3, true, false>(p, grid, stream, g);
     }
   }
   if (slices > 1) {

@@ -15,9 +15,9 @@ namespace {
 struct GradArgs {
   const uint16_t *F, *S;       // first operand [k][f]; second [s][k] (dX) or [k][s] (dW)
   int64_t ldf, lds;            // their rows' elements
-  int64_t nk, slice;           // k; k of a slice (a multiple of 32)
+  int64_t nk, slice;           // k; k of a slice (a multiple of 64)
   int64_t ns;                  // rows of the result
-  int nf, ta, tb, grid;        // its columns; tiles along both; workgroups of a slice
+  int nf, ta, tb;              // its columns; tiles along both
   const uint8_t *mc, *ms;      // mask
   int64_t mrow, msrow;
   void* Y;
@@ -25,59 +25,117 @@ struct GradArgs {
   int accumulate, vec;
 };
 
-// 4 consecutive columns' masks: zero where the mask's value is not > 0 (c a multiple of 4, below the row's padding)
-template <int MASK, int V>
-__device__ __forceinline__ void apply_mask(const GradArgs& g, int64_t row, int c, float (&v)[V]) {
-  const uint32_t scale = g.ms[row * g.msrow + (c >> 5)];
-#pragma unroll
-  for (int q = 0; q < V; ++q) {
-    uint32_t code;
-    bool pos;
-    if (MASK == 1) {
-      code = (uint32_t)*reinterpret_cast<const uint16_t*>(g.mc + row * g.mrow + ((c + (q & ~3)) >> 1)) >> (4 * (q & 3)) & 15u;
-      pos = code >= 1u && code <= 7u;
-    } else {
-      code = *reinterpret_cast<const uint32_t*>(g.mc + row * g.mrow + c + (q & ~3)) >> (8 * (q & 3)) & 255u;
-      pos = code >= 1u && code <= 0x7Eu;
-    }
-    if (!pos || scale == 255u) v[q] = 0.f;
-  }
+// Codes of the mask's 4 consecutive columns from c on (a multiple of 4, below the row's padding)
+template <int MASK>
+__device__ __forceinline__ uint32_t mask_codes(const GradArgs& g, int64_t row, int c) {
+  if (MASK == 1) return *reinterpret_cast<const uint16_t*>(g.mc + row * g.mrow + (c >> 1));
+  return *reinterpret_cast<const uint32_t*>(g.mc + row * g.mrow + c);
 }
 
-template <bool GRAD_INPUT, bool YBF16, int MASK, int WA, int WB, int MB, int NB, int NSTG, int OCC>
+// whether the mask's value at one of them is > 0, its block being finite
+template <int MASK>
+__device__ __forceinline__ bool mask_open(uint32_t codes, int q) {
+  if (MASK == 1) return (codes >> (4 * q) & 15u) - 1u < 7u;
+  return (codes >> (8 * q) & 255u) - 1u < 0x7Eu;
+}
+
+// zero where the mask's value is not > 0
+template <int MASK>
+__device__ __forceinline__ float masked(const GradArgs& g, int64_t row, int c, float v) {
+  if constexpr (MASK != 0) {
+    const uint32_t codes = mask_codes<MASK>(g, row, c & ~3);
+    if (g.ms[row * g.msrow + (c >> 5)] == 255 || !mask_open<MASK>(codes, c & 3)) v = 0.f;
+  }
+  return v;
+}
+template <int MASK, int V, int IT>
+struct StoreMasked {
+  const GradArgs& g;
+  uint32_t codes[2][IT][V / 4], scale[2][IT];
+  __device__ __forceinline__ void columns(int) {}
+  __device__ __forceinline__ void row(int set, int it, int64_t row, int c) {
+    if constexpr (MASK != 0) {
+      scale[set][it] = g.ms[row * g.msrow + (c >> 5)];
+#pragma unroll
+      for (int p = 0; p < V; p += 4) codes[set][it][p / 4] = mask_codes<MASK>(g, row, c + p);
+    }
+  }
+  // The loads end here whatever path follows: one left in flight would make the compiler wait for all transfers in the
+  // next tile's loop.
+  __device__ __forceinline__ void settle(int set) {
+    if constexpr (MASK != 0) {
+#pragma unroll
+      for (int it = 0; it < IT; ++it) {
+        asm volatile("" : "+v"(scale[set][it]));
+#pragma unroll
+        for (int p = 0; p < V / 4; ++p) asm volatile("" : "+v"(codes[set][it][p]));
+      }
+    }
+  }
+  __device__ __forceinline__ float one(int64_t row, int c, float v) { return masked<MASK>(g, row, c, v); }
+  __device__ __forceinline__ void finish(int set, int it, float (&v)[V]) {
+    if constexpr (MASK != 0) {
+#pragma unroll
+      for (int q = 0; q < V; ++q) {
+        const uint32_t k = scale[set][it] == 255 ? 0u : codes[set][it][q >> 2];
+        if (!mask_open<MASK>(k, q & 3)) v[q] = 0.f;
+      }
+    }
+  }
+};
+
+template <bool GRAD_INPUT, bool YBF16, int MASK, int WA, int WB, int MB, int NB, int OCC>
 __global__ __launch_bounds__(256, OCC) void k_mx_grad(const GradArgs g) {
-  using T = TileProduct<K_BF16T, GRAD_INPUT ? K_BF16 : K_BF16T, WA, WB, MB, NB, NSTG, false>;
+  using T = TileProduct<K_BF16T, GRAD_INPUT ? K_BF16 : K_BF16T, WA, WB, MB, NB, false>;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS];
+  TileOrder order;
+  order.init(blockIdx.x, gridDim.x, g.ta, g.tb);
   int ia, ib;
-  if (!tile_of(blockIdx.x, g.grid, g.ta, g.tb, ia, ib)) return;
-  const int f0 = ia * WA;
-  const int64_t s0 = (int64_t)ib * WB;
+  if (!order.get(0, ia, ib)) return;
   const int64_t k0 = blockIdx.y * g.slice, nk = min(g.slice, g.nk - k0);
-  const int stages = (int)((nk + 31) / 32);
+  const int stages = (int)((nk + 63) / 64);
   T t;
-  t.init(lds);
-  // bytes from a tile's first element to the end of its last row (rounded up to whole 16-byte chunks)
-  t.a.mem.init(g.F + k0 * g.ldf + f0, ((nk - 1) * g.ldf + ((g.nf + 7) / 8 * 8 - f0)) * 2, (int)(32 * g.ldf * 2), stages);
-  t.a.init(g.ldf * 2, t.wave, t.lane, t.wa, g.nf - f0);
-  if (GRAD_INPUT) {
-    const int64_t rows = min((int64_t)WB, g.ns - s0);
-    t.b.mem.init(g.S + s0 * g.lds + k0, ((rows - 1) * g.lds + (int64_t)stages * 32) * 2, 64, stages);
-    t.b.init(g.lds * 2, t.wave, t.lane, t.wb, 0);
-  } else {
-    t.b.mem.init(g.S + k0 * g.lds + s0, ((nk - 1) * g.lds + ((g.ns + 7) / 8 * 8 - s0)) * 2, (int)(32 * g.lds * 2), stages);
-    t.b.init(g.lds * 2, t.wave, t.lane, t.wb, g.ns - s0);
+  t.init(lds, 0);
+  t.a.init(g.ldf * 2, t.wave, t.lane, t.wa);
+  t.b.init(g.lds * 2, t.wave, t.lane, t.wb);
+  t.tail = 0;
+  // bytes from a tile's first element to the end of its last row, rounded up to whole 16-byte chunks; what a tile reads
+  // behind a row's end before that only reaches results that are not stored
+  auto locate = [&](bool any, Stretch& a, Stretch& b) {
+    const int f0 = ia * WA, n = any ? stages : 0;
+    const int64_t s0 = (int64_t)ib * WB;
+    a.init(g.F + k0 * g.ldf + f0, ((nk - 1) * g.ldf + ((g.nf + 7) / 8 * 8 - f0)) * 2, (int)(64 * g.ldf * 2), n);
+    if (GRAD_INPUT) {
+      const int64_t rows = min((int64_t)WB, g.ns - s0);
+      b.init(g.S + s0 * g.lds + k0, ((rows - 1) * g.lds + (int64_t)stages * 64) * 2, T::B::STEP, n);
+    } else {
+      b.init(g.S + k0 * g.lds + s0, ((nk - 1) * g.lds + ((g.ns + 7) / 8 * 8 - s0)) * 2, (int)(64 * g.lds * 2), n);
+    }
+  };
+  locate(true, t.a.mem, t.b.mem);
+  t.start();
+  bool more = true;
+  for (int r = 1; more; ++r) {
+    const int64_t row0 = (int64_t)ib * WB + t.wb;
+    const int c0 = ia * WA + t.wa;
+    more = order.get(r, ia, ib);
+    locate(more, t.an, t.bn);
+    t.multiply(max(2, stages));
+    if (!T::STAYS) wait_and_barrier<0>();
+    uint8_t* buf = T::STAYS ? lds + T::LDS - 4 * 4096 * T::PB : lds;
+    if (gridDim.y > 1) {
+      float* part = static_cast<float*>(g.Y) + blockIdx.y * g.ns * (int64_t)g.nf;
+      store_rows<false, T::PB>(t.acc, buf, part, g.nf, row0, g.ns, c0, g.nf, g.vec, false, StoreAsIs());
+    } else {
+      constexpr int V = YBF16 ? 8 : 4;
+      constexpr int PB = MASK != 0 && !YBF16 ? 1 : T::PB;  // fewer rows at a time where each brings a mask's registers too
+      StoreMasked<MASK, V, 16 * PB / V> done = {g, {}, {}};
+      store_rows<YBF16, PB>(t.acc, buf, g.Y, g.ld, row0, g.ns, c0, g.nf, g.vec, g.accumulate, done);
+    }
+    if (!T::STAYS) return;
+    t.clear();
   }
-  t.run(stages);
-  const int64_t row0 = s0 + t.wb;
-  const int c0 = f0 + t.wa;
-  if (gridDim.y > 1) {
-    float* part = static_cast<float*>(g.Y) + blockIdx.y * g.ns * (int64_t)g.nf;
-    store_rows<false>(t.acc, lds, part, g.nf, row0, g.ns, c0, g.nf, g.vec, false, [](int64_t, int, auto&) {});
-  } else {
-    store_rows<YBF16>(t.acc, lds, g.Y, g.ld, row0, g.ns, c0, g.nf, g.vec, g.accumulate, [&](int64_t row, int c, auto& v) {
-      if constexpr (MASK != 0) apply_mask<MASK>(g, row, c, v);
-    });
-  }
+  wait_and_barrier<0>();  // nothing may still be writing LDS when the workgroup ends
 }
 
 // The slices' partial products, added in their order; mask, accumulation and the result's type. Four columns a thread.
@@ -93,7 +151,9 @@ __global__ __launch_bounds__(256) void k_mx_grad_join(const GradArgs g, const fl
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         if (c + q < g.nf) v[q] += part[s * stride + row * g.nf + c + q];
-    if constexpr (MASK != 0) apply_mask<MASK>(g, row, c, v);
+    StoreMasked<MASK, 4, 1> done = {g, {}, {}};
+    done.row(0, 0, row, c);
+    done.finish(0, 0, v);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       if (c + q >= g.nf) continue;
@@ -107,7 +167,7 @@ __global__ __launch_bounds__(256) void k_mx_grad_join(const GradArgs g, const fl
   }
 }
 
-// dY with rows of kp (a multiple of 32) columns, zeros behind the last
+// dY with rows of kp (a multiple of 64) columns, zeros behind the last
 __global__ __launch_bounds__(256) void k_pad_rows(const uint16_t* __restrict__ X, int64_t ld, int64_t n, int cols, int kp,
                                                   uint16_t* __restrict__ Y) {
   const int64_t total = n * (kp / 8);
@@ -161,13 +221,13 @@ struct GradPlan {
 };
 
 GradPlan grad_plan(int64_t ns, int64_t nf, int64_t nk) {
-  GradPlan p = {0, 1, std::max<int64_t>(32, (int64_t)align_up(nk, 32))};
+  GradPlan p = {0, 1, std::max<int64_t>(64, (int64_t)align_up(nk, 64))};
   auto tiles = [&](int64_t w) { return ceil_div(ns, w) * ceil_div(nf, w); };
   p.tile = tiles(256) >= 192 ? 2 : tiles(128) >= 192 ? 1 : 0;
   const int64_t t = tiles(64 << p.tile);
   if (t > 0 && t < 192) {
     const int64_t s = std::max<int64_t>(1, std::min<int64_t>({512 / t, ceil_div(nk, 256), 64}));
-    p.slice = std::max<int64_t>(32, (int64_t)align_up(ceil_div(nk, s), 32));
+    p.slice = std::max<int64_t>(64, (int64_t)align_up(ceil_div(nk, s), 64));
   }
   p.slices = (int)std::max<int64_t>(1, ceil_div(nk, p.slice));
   return p;
@@ -179,9 +239,12 @@ size_t grad_part_bytes(const GradPlan& p, int64_t ns, int64_t nf) {
 
 template <bool GI, bool B, int M>
 void grad_go(int tile, dim3 grid, hipStream_t stream, const GradArgs& g) {
-  if (tile == 2) hipLaunchKernelGGL((k_mx_grad<GI, B, M, 256, 256, 4, 4, 4, 1>), grid, dim3(256), 0, stream, g);
-  else if (tile == 1) hipLaunchKernelGGL((k_mx_grad<GI, B, M, 128, 128, 2, 2, 5, 2>), grid, dim3(256), 0, stream, g);
-  else hipLaunchKernelGGL((k_mx_grad<GI, B, M, 64, 64, 1, 1, 5, 3>), grid, dim3(256), 0, stream, g);
+#define GPTQ_GO(WA, WB, MB, NB, OCC) \
+  hipLaunchKernelGGL((k_mx_grad<GI, B, M, WA, WB, MB, NB, OCC>), grid, dim3(256), 0, stream, g)
+  if (tile == 2) GPTQ_GO(256, 256, 4, 4, 1);
+  else if (tile == 1) GPTQ_GO(128, 128, 2, 2, 2);
+  else GPTQ_GO(64, 64, 1, 1, 3);
+#undef GPTQ_GO
 }
 
 template <bool GI, bool B, int M>
@@ -191,8 +254,7 @@ hipError_t grad_run(const GradPlan& p, GradArgs g, float* part, hipStream_t stre
   g.ta = (int)ceil_div(g.nf, 64 << p.tile);
   if (p.slices > 1) g.Y = part, g.ld = g.nf, g.vec = g.nf % 4 == 0;
   g.tb = (int)ceil_div(g.ns, 64 << p.tile);
-  g.grid = (int)tile_grid((int64_t)g.ta * g.tb);
-  grad_go<GI, B, M>(p.tile, dim3((unsigned)g.grid, (unsigned)p.slices), stream, g);
+  grad_go<GI, B, M>(p.tile, dim3(tile_grid((int64_t)g.ta * g.tb, p.tile == 2 ? 256 : 1 << 30), (unsigned)p.slices), stream, g);
   if (p.slices > 1)
     hipLaunchKernelGGL((k_mx_grad_join<B, M>), dim3((unsigned)std::min<int64_t>(2048, ceil_div(g.ns * ceil_div(g.nf, 4), 256))),
                        dim3(256), 0, stream, fin, part, p.slices);
@@ -202,7 +264,7 @@ hipError_t grad_run(const GradPlan& p, GradArgs g, float* part, hipStream_t stre
 // The tile product reads dY with 16-byte loads of whole chunks; where rows are not aligned, or a row's tail would
 // bring its neighbour's numbers into the sum (dX), a padded copy is read instead.
 bool dy_direct(const uint16_t* dY, int64_t ld, int64_t out, bool sum_over_out) {
-  return vec_rows(dY, ld, GPTQ_BF16) && ld <= ((int64_t)1 << 20) && (!sum_over_out || out % 32 == 0);
+  return vec_rows(dY, ld, GPTQ_BF16) && ld <= ((int64_t)1 << 20) && (!sum_over_out || out % 64 == 0);
 }
 
 constexpr int64_t ROWS_MAX = (int64_t)1 << 20;  // rows of dX a launch

@@ -2,19 +2,22 @@
 // k of a(i, k) b(j, k), operands streaming from memory straight into a ring of LDS stages while the matrix cores work
 // on earlier ones.
 //
-// What bounds it is LDS: a 32 x 32 product of two fragments reads both of them, 2 KB, for 32 cycles of the matrix
-// core (bf16 and 4-bit elements). A wave of 128 x 128 reads 8 fragments for 16 products, 16 B per matrix-core cycle and
-// wave, half of what 32 x 32 products one by one would take; with 128 x 64 waves it is 24 B, and LDS becomes the limit.
-// That leaves one wave to a SIMD (256 accumulators), so nothing but its own instruction order hides latency:
-// a stage holds two steps of k; the fragments of the second are read between the products of the first, the next
-// stage's first fragments between those of the second, and the wait for the next stage with its barrier lies in the
-// middle, where products are queued on both sides.
+// What bounds it: LDS and the L2. A 32 x 32 product of two fragments reads both of them, 2 KB, for 32 cycles of the
+// matrix core (bf16 and 4-bit elements). A wave of 128 x 128 reads 8 fragments for 16 products, 16 B per matrix-core
+// cycle and wave, half of what 32 x 32 products one by one would take. That leaves one wave to a SIMD (256 accumulators),
+// so nothing but its own instruction order hides latency. The L2 hands out lines of 128 bytes whatever part is asked
+// for: a stage therefore takes whole lines, 128 bytes of each row (64 bytes of each row, twice, cost 2.5 times the
+// lines of the 4-bit product at 16384 x 4096 x 11008 with its scales, 16 TB/s, which was the limit).
 //
-// Stage layout. Operands whose k runs along a row (E2M1, E4M3, bf16) keep each row's piece of the stage (64 or 128
-// bytes) together; the 16-byte chunks of row r are permuted by XOR with bits of the Gray code of r, so that the 16
-// consecutive rows that one ds_read_b128 takes at one logical chunk lie on different banks. Operands whose k runs
-// down the columns (bf16, "T") keep each k's row together and are read by the transposing ds_read_b64_tr_b16;
-// chunks are permuted by bits of k.
+// A stage holds four steps of k (64 columns each for MX, 16 for bf16), two stages make the ring. The fragments of a step
+// are read between the products of the step before. Before the last step of a stage its buffer has been read by all
+// waves and the next stage has arrived (one wait, one barrier); between its products go the first fragments of the next
+// stage and the transfers of the stage after that, which have until the next such point to land.
+//
+// Stage layout. Operands whose k runs along a row (E2M1, E4M3, bf16) keep 128 bytes of each row together (E4M3: two such
+// planes); the 16-byte chunks of row r are permuted by XOR with the Gray code of r, so that the consecutive rows that
+// one ds_read_b128 takes at one logical chunk lie on different banks. Operands whose k runs down the columns (bf16, "T")
+// keep each k's row together and are read by the transposing ds_read_b64_tr_b16; chunks are permuted by bits of k.
 #pragma once
 
 #include <utility>
@@ -47,6 +50,14 @@ __device__ __forceinline__ void dma16(const i32x4& rsrc, uint32_t lds_addr, uint
                : "s"(lds_addr), "v"(voff), "s"(rsrc)
                : "memory", "m0");
 }
+// the same where `skip` is 0; a branch of the compiler's would let it move products across the ring's barriers
+__device__ __forceinline__ void dma16_unless(int skip, const i32x4& rsrc, uint32_t lds_addr, uint32_t voff) {
+  asm volatile("s_cmp_lg_u32 %3, 0\n\ts_cbranch_scc1 .Lno_transfer%=\n\ts_mov_b32 m0, %0\n\t"
+               "buffer_load_dwordx4 %1, %2, 0 offen lds\n.Lno_transfer%=:"
+               :
+               : "s"(lds_addr), "v"(voff), "s"(rsrc), "s"(skip)
+               : "memory", "m0", "scc");
+}
 #pragma clang diagnostic pop
 
 // every LDS read of this wave has its data and at most N transfers are still in flight; then the workgroup's barrier
@@ -56,47 +67,50 @@ __device__ __forceinline__ void wait_and_barrier() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
 }
 
+__device__ __forceinline__ int64_t uniform64(int64_t v) {
+  return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v) |
+                   (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)((uint64_t)v >> 32)) << 32);
+}
+
 // A stretch of memory that advances by `step` bytes from stage to stage; reads past its end, and those of stages past
-// the last one, give zeros.
+// the last one, give zeros. All members are the same in all lanes.
 struct Stretch {
   uint64_t addr;
   int64_t left;
   int step, stages;
-  i32x4 rsrc;
-  // every argument is the same in all lanes
   __device__ __forceinline__ void init(const void* p, int64_t bytes, int st, int n) {
-    addr = (uint64_t)(uintptr_t)p;
-    addr = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)addr) |
-           (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(addr >> 32)) << 32;
-    left = (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)bytes) |
-                     (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)((uint64_t)bytes >> 32)) << 32);
+    addr = (uint64_t)uniform64((int64_t)(uintptr_t)p), left = uniform64(bytes);
     step = __builtin_amdgcn_readfirstlane(st), stages = __builtin_amdgcn_readfirstlane(n);
-    set();
   }
-  __device__ __forceinline__ void set() {
+  __device__ __forceinline__ i32x4 rsrc() const {
     const int hi = (int)(left >> 31);  // 0 where 0 <= left < 2^31
     const int n = stages <= 0 || hi < 0 ? 0 : hi > 0 ? 0x7FFFFFF0 : (int)left;
-    rsrc = (i32x4){(int)(uint32_t)addr, (int)(uint32_t)(addr >> 32) & 0xFFFF, n, 0x00020000};
+    return (i32x4){(int)(uint32_t)addr, (int)(uint32_t)(addr >> 32) & 0xFFFF, n, 0x00020000};
   }
-  __device__ __forceinline__ void advance() {
-    addr += (uint64_t)step, left -= step, --stages;
-    set();
+  __device__ __forceinline__ void advance() { addr += (uint64_t)step, left -= step, --stages; }
+  __device__ __forceinline__ void take_if(bool c, const Stretch& s) {
+    addr = c ? s.addr : addr, left = c ? s.left : left, stages = c ? s.stages : stages;
+  }
+  __device__ __forceinline__ Stretch at(int steps) const {
+    Stretch s = *this;
+    s.addr += (uint64_t)steps * (uint32_t)step, s.left -= (int64_t)steps * step;
+    return s;
   }
 };
 
-// XOR pattern of a row's 16-byte chunks: 4 chunks (64-byte rows) or 8 (128-byte rows)
-__device__ __forceinline__ int swz4(int r) { return ((r >> 1) ^ (r >> 2)) & 3; }
+// XOR patterns of a row's 16-byte chunks: 2 chunks (32-byte rows) or 8 (128-byte rows)
+__device__ __forceinline__ int swz2(int r) { return (r >> 3) & 1; }
 __device__ __forceinline__ int swz8(int r) { return (r ^ (r >> 1)) & 7; }
 
 // One operand: W rows (columns of a T operand) of the tile, transferred by NW waves.
 template <int KIND, int W, int NW>
 struct Operand {
-  static constexpr int ROW = KIND == K_E4M3 ? 128 : 64;   // bytes of a row in a stage (of 32 k of a T column)
-  static constexpr int BYTES = ROW * W;
+  static constexpr int PLANES = KIND == K_E4M3 ? 2 : 1;
+  static constexpr int BYTES = 128 * PLANES * W;
   static constexpr int NI = BYTES / 1024 / NW;            // transfers per wave and stage
   static constexpr int FRAG = KIND == K_E4M3 ? 8 : 4;     // registers of a fragment
-  static constexpr int NB = KIND == K_E4M3 ? 4 : KIND == K_BF16T ? 4 : 2;
-  static_assert(NI >= 1 && BYTES % (1024 * NW) == 0, "tile too narrow for its waves");
+  static constexpr int STEP = 128 * PLANES;               // bytes along a row per stage (not T)
+  static_assert(BYTES % (1024 * NW * PLANES) == 0, "tile too narrow for its waves");
   static_assert(KIND != K_BF16T || W >= 64, "the T layout's permutation needs 8 chunks");
 
   // XOR pattern of a k row's chunks in the T layout: the four rows that a transposing read touches (64 bytes each) lie
@@ -104,52 +118,54 @@ struct Operand {
   static __device__ __forceinline__ int swzt(int k) { return W >= 128 ? (k & 3) << 2 : (k & 2) << 1; }
 
   Stretch mem;
+  i32x4 rsrc;          // of the stage whose transfers are being issued
+  uint32_t beyond;     // E4M3: set where that stage's second plane lies behind the row's end
   uint32_t voff[NI];   // this lane's offsets from mem.addr
-  uint32_t roff[NB];   // this lane's fragment offsets within a stage
+  uint32_t roff[4];    // this lane's fragment offsets within a stage
 
-  // row_bytes: distance of rows (of k rows for T); cols: columns of a T operand from its first one on
-  __device__ __forceinline__ void init(int64_t row_bytes, int wave, int lane, int w0, int64_t cols) {
+  // row_bytes: distance of rows (of k rows for T)
+  __device__ __forceinline__ void init(int64_t row_bytes, int wave, int lane, int w0) {
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const int p = wave * NI + i;
+      const int p = wave * (NI / PLANES) + i % (NI / PLANES);
       if (KIND == K_BF16T) {
         const int k = p * (512 / W) + lane / (W / 8);
         const int q = (lane % (W / 8)) ^ swzt(k);
-        voff[i] = 8 * q < cols ? (uint32_t)(k * row_bytes + q * 16) : 0x80000000u;
-      } else if (KIND == K_E4M3) {
-        const int row = p * 8 + (lane >> 3);
-        voff[i] = (uint32_t)(row * row_bytes + ((lane & 7) ^ swz8(row)) * 16);
+        voff[i] = (uint32_t)(k * row_bytes + q * 16);
       } else {
-        const int row = p * 16 + (lane >> 2);
-        voff[i] = (uint32_t)(row * row_bytes + ((lane & 3) ^ swz4(row)) * 16);
+        const int row = p * 8 + (lane >> 3);
+        voff[i] = (uint32_t)(row * row_bytes + ((lane & 7) ^ swz8(row)) * 16 + i / (NI / PLANES) * 128);
       }
     }
     const int r = lane & 31, h = lane >> 5;
-    if (KIND == K_BF16T) {
-      const int g = lane >> 4, s = lane & 15;
-      const int k = 8 * (g >> 1) + (s >> 2);
+    const int g = lane >> 4, s = lane & 15, k = 8 * (g >> 1) + (s >> 2);
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const int c = (b * 32) + 16 * (g & 1) + (s & 3) * 4;
-        roff[b] = (uint32_t)(k * (2 * W) + ((((w0 + c) >> 3) ^ swzt(k)) << 4) + (c & 7) * 2);
-      }
-    } else if (KIND == K_E4M3) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int chunk = 4 * (q >> 1) + 2 * (q & 1) + h;
+    for (int q = 0; q < 4; ++q) {
+      if (KIND == K_BF16T) {  // block q of 32 columns
+        const int c = w0 + q * 32 + 16 * (g & 1) + (s & 3) * 4;
+        roff[q] = (uint32_t)(k * (2 * W) + (((c >> 3) ^ swzt(k)) << 4) + (c & 7) * 2);
+      } else {                // E4M3: step q / 2 of a plane, half q % 2 of the fragment; else step q
+        const int chunk = KIND == K_E4M3 ? 4 * (q >> 1) + 2 * (q & 1) + h : 2 * q + h;
         roff[q] = (uint32_t)((w0 + r) * 128 + (chunk ^ swz8(r)) * 16);
       }
-    } else {
-#pragma unroll
-      for (int q = 0; q < 2; ++q) roff[q] = (uint32_t)((w0 + r) * 64 + ((2 * q + h) ^ swz4(r)) * 16);
     }
   }
 
-  __device__ __forceinline__ void transfer(int i, uint32_t lds_addr, int wave) const {
-    dma16(mem.rsrc, (uint32_t)__builtin_amdgcn_readfirstlane((int)(lds_addr + (wave * NI + i) * 1024)), voff[i]);
+  // the next transfers are those of the stage at mem; tail: the last stage's second plane lies behind the row's end
+  __device__ __forceinline__ void open(int tail) {
+    rsrc = mem.rsrc();
+    beyond = mem.stages == 1 && tail ? 0x80000000u : 0u;
   }
 
-  // fragment of 32 rows (block b of the wave's) at step J of the stage
+  // the i-th transfer of the stage
+  __device__ __forceinline__ void transfer(int i, uint32_t lds_addr, int wave) const {
+    constexpr int PER_PLANE = NI / PLANES;
+    const uint32_t v = KIND == K_E4M3 && i >= PER_PLANE ? voff[i] | beyond : voff[i];
+    const int at_lds = (i / PER_PLANE) * (W * 128) + (wave * PER_PLANE + i % PER_PLANE) * 1024;
+    dma16(rsrc, (uint32_t)__builtin_amdgcn_readfirstlane((int)(lds_addr + at_lds)), v);
+  }
+
+  // fragment of 32 rows (block B of the wave's) at step J of the stage
   template <int J, int B>
   __device__ __forceinline__ void read(const uint8_t* stage, int (&f)[FRAG]) const {
     if constexpr (KIND == K_BF16T) {
@@ -161,7 +177,8 @@ struct Operand {
     } else {
 #pragma unroll
       for (int q = 0; q < FRAG / 4; ++q) {
-        const i32x4 v = *reinterpret_cast<const i32x4*>(stage + roff[J * (FRAG / 4) + q] + B * 32 * ROW);
+        const int at = KIND == K_E4M3 ? (J >> 1) * (W * 128) : 0;
+        const i32x4 v = *reinterpret_cast<const i32x4*>(stage + roff[KIND == K_E4M3 ? (J & 1) * 2 + q : J] + at + B * 4096);
 #pragma unroll
         for (int i = 0; i < 4; ++i) f[4 * q + i] = v[i];
       }
@@ -193,43 +210,63 @@ __device__ __forceinline__ i32x8 as_operand(const int (&f)[N]) {
 
 // A (first operand) x B (second): KA is K_E2M1 with KB K_E2M1 or K_E4M3, or both are bf16 kinds.
 // SPLIT: E4M3 fragments in two parts (see split_e4m3).
-template <int KA, int KB, int WA, int WB, int MB, int NB, int NSTG, bool SPLIT>
+template <int KA, int KB, int WA, int WB, int MB, int NB, bool SPLIT>
 struct TileProduct {
   static constexpr int NW = 4;
   static constexpr bool MX = KA == K_E2M1;
   static constexpr int WAVES_A = WA / (32 * MB), WAVES_B = WB / (32 * NB);
-  static_assert(WAVES_A * WAVES_B == NW && NSTG >= 3, "four waves, three stages at least");
-  static_assert(!MX || NSTG <= 4, "a scale buffer is refilled NSTG - 1 stages ahead and read four stages long");
+  static_assert(WAVES_A * WAVES_B == NW, "four waves");
   using A = Operand<KA, WA, NW>;
   using B = Operand<KB, WB, NW>;
   static constexpr int STAGE = A::BYTES + B::BYTES;
-  static constexpr int SCALES = MX ? (WA + WB) * 16 : 0;         // 512 columns' scale bytes
-  static constexpr int STORE = NW * 32 * (32 * MB + 4) * 4;      // what store_rows needs
-  static constexpr int LDS = NSTG * STAGE + SCALES > STORE ? NSTG * STAGE + SCALES : STORE;
-  static constexpr int SI = MX ? (WA + WB) / 64 : 0;             // scale transfers per 512 columns
-  static constexpr int SC = (SI + NW - 1) / NW;                  // per wave (the last ones may repeat the first)
+  // Scale bytes are held for 1024 columns (32 bytes of each row), refilled when the last 512 of them are in registers.
+  static constexpr int SCALES = MX ? (WA + WB) * 32 : 0;
+  // The large tiles' workgroups stay for several tiles, and a tile's results leave through memory of their own while the
+  // ring fills with the next one's first stages; the small ones', of which several share a CU, through the ring's.
+  static constexpr bool STAYS = MB == 4;
+  static constexpr int PB = STAYS && !MX ? 2 : 1;
+  static constexpr int LDS = 2 * STAGE + SCALES + (STAYS ? NW * 4096 * PB : 0);
+  static constexpr int SI = MX ? ((WA + WB) / 32 + NW - 1) / NW : 0;  // scale transfers per wave (some twice)
   static constexpr int PER = A::NI + B::NI;
   static constexpr int NM = MB * NB;
-  static_assert(!MX || (WA % 64 == 0 && WB % 64 == 0), "scale transfers take 64 rows");
+  // Share of a stage's transfers issued by the end of the last step of the stage two before it, then of the next one's first
+  // and second. All of them between the last step's products saturate the L1's 64 bytes a cycle while the matrix cores
+  // wait (16384 x 4096 x 11008 in 4 bits: 478 us, against 444); spread over all four steps the last ones arrive late (455).
+  static constexpr int D3 = PER * 6 / 16, D0 = PER * 11 / 16, D1 = PER;
+  static_assert(!MX || (WA % 64 == 0 && WB % 64 == 0), "scale transfers");
 
   A a;
   B b;
-  Stretch sa, sb;
-  int64_t srow;      // bytes of a scale row
+  Stretch sa, sb;              // scale bytes of the tile
+  Stretch an, bn, san, sbn;    // the next tile's operands and scale bytes
+  int tail;                    // E4M3: the row's last stage ends after its first plane
   uint8_t* lds;
   uint32_t base;     // LDS address of lds
   int wave, lane, wa, wb;
-  uint32_t slot_w, slot_r;
+  uint32_t slot;     // offset of the stage being multiplied
+  uint32_t svoff[SI ? SI : 1], soff;
+  int stile[SI ? SI : 1];
   f32x16 acc[MB][NB];
   int fa[2][MB][A::FRAG], fb[2][NB][B::FRAG];
-  int sca[MB][4], scb[NB][4], nca[MB][4], ncb[NB][4];
+  int sca[MB][2], scb[NB][2], nca[MB][4], ncb[NB][4];
 
-  __device__ __forceinline__ void init(uint8_t* l) {
+  __device__ __forceinline__ void init(uint8_t* l, int64_t srow) {
     lds = l, base = (uint32_t)(uintptr_t)l;
     lane = threadIdx.x & 63;
     wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     wa = (wave / WAVES_B) * (32 * MB), wb = (wave % WAVES_B) * (32 * NB);
-    slot_w = slot_r = 0;
+    slot = 0;
+#pragma unroll
+    for (int i = 0; i < SI; ++i) {
+      stile[i] = (wave * SI + i) % ((WA + WB) / 32);
+      const int row = 32 * stile[i] + (lane >> 1);
+      svoff[i] = (uint32_t)((row < WA ? row : row - WA) * srow + ((lane & 1) ^ swz2(row)) * 16);
+    }
+    soff = (uint32_t)(2 * STAGE + (lane & 31) * 32 + swz2(lane) * 16);
+    clear();
+  }
+
+  __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int i = 0; i < MB; ++i)
 #pragma unroll
@@ -238,48 +275,59 @@ struct TileProduct {
         for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
   }
 
-  static __device__ __forceinline__ uint32_t next_slot(uint32_t s) { return s + STAGE == NSTG * STAGE ? 0u : s + STAGE; }
-
-  __device__ __forceinline__ void transfer_scales() {
+  // the scale bytes of 1024 columns, where `skip` is 0
+  __device__ __forceinline__ void transfer_scales(int skip, const Stretch& ga, const Stretch& gb) {
+    const i32x4 ra = ga.rsrc(), rb = gb.rsrc();
 #pragma unroll
-    for (int i = 0; i < SC; ++i) {
-      const int t = (wave + NW * i) % (SI ? SI : 1);
-      const bool second = t >= WA / 64;
-      const uint32_t v = (uint32_t)((64 * (second ? t - WA / 64 : t) + lane) * srow);
-      dma16(second ? sb.rsrc : sa.rsrc, (uint32_t)__builtin_amdgcn_readfirstlane((int)(base + NSTG * STAGE + t * 1024)), v);
-    }
-    sa.advance(), sb.advance();
-  }
-
-  // the i-th of a stage's PER transfers
-  __device__ __forceinline__ void transfer(int i) {
-    if (i < A::NI) a.transfer(i, base + slot_w, wave);
-    else b.transfer(i - A::NI, base + slot_w + A::BYTES, wave);
-    if (i == PER - 1) {
-      a.mem.advance(), b.mem.advance();
-      slot_w = next_slot(slot_w);
+    for (int i = 0; i < SI; ++i) {
+      dma16_unless(skip, 32 * stile[i] < WA ? ra : rb,
+                   (uint32_t)__builtin_amdgcn_readfirstlane((int)(base + 2 * STAGE + stile[i] * 1024)), svoff[i]);
     }
   }
 
-  // the t-th of the MB + NB fragments of step J of the stage at slot_r into set SET
+  // the i-th of a stage's PER transfers, into the ring's half at `to`
+  __device__ __forceinline__ void transfer(int i, uint32_t to) {
+    if (i == 0) a.open(0), b.open(tail);
+    if (i < A::NI) a.transfer(i, base + to, wave);
+    else b.transfer(i - A::NI, base + to + A::BYTES, wave);
+    if (i == PER - 1) a.mem.advance(), b.mem.advance();
+  }
+
+  // the t-th of the MB + NB fragments of step J of the stage at `from` into set SET
   template <int SET, int J, int T>
-  __device__ __forceinline__ void read_frag() {
-    if constexpr (T < MB) a.template read<J, T>(lds + slot_r, fa[SET][T]);
-    else b.template read<J, T - MB>(lds + slot_r + A::BYTES, fb[SET][T - MB]);
+  __device__ __forceinline__ void read_frag(uint32_t from) {
+    if constexpr (T < MB) a.template read<J, T>(lds + from, fa[SET][T]);
+    else b.template read<J, T - MB>(lds + from + A::BYTES, fb[SET][T - MB]);
   }
 
-  template <int T>
-  __device__ __forceinline__ void read_scale() {
-    const int row = (T < MB ? wa + 32 * T : WA + wb + 32 * (T - MB)) + (lane & 31);
-    const i32x4 v = *reinterpret_cast<const i32x4*>(lds + NSTG * STAGE + row * 16);
+  // scale bytes of stages `at` (even) and at + 1, 16 of each row
+  __device__ __forceinline__ void read_scales(int at) {
+    const uint8_t* p = lds + (soff ^ (uint32_t)((at >> 1 & 1) * 16));
+    static_for<0, MB + NB>([&](auto t) {
+      constexpr int T = decltype(t)::value;
+      const i32x4 v = *reinterpret_cast<const i32x4*>(p + (T < MB ? wa + 32 * T : WA + wb + 32 * (T - MB)) * 32);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if constexpr (T < MB) nca[T][q] = v[q];
-      else ncb[T - MB][q] = v[q];
+      for (int q = 0; q < 4; ++q) {
+        if constexpr (T < MB) nca[T][q] = v[q];
+        else ncb[T - MB][q] = v[q];
+      }
+    });
+  }
+
+  // those of the pair's stage P into the products' registers; lanes 32..63 take the odd blocks' bytes
+  template <int P>
+  __device__ __forceinline__ void take_scales() {
+    const int sh = 8 * (lane >> 5);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+#pragma unroll
+      for (int m = 0; m < MB; ++m) sca[m][q] = (int)((uint32_t)nca[m][2 * P + q] >> sh);
+#pragma unroll
+      for (int n = 0; n < NB; ++n) scb[n][q] = (int)((uint32_t)ncb[n][2 * P + q] >> sh);
     }
   }
 
-  template <int SET, int Q, int J, int M, int N>
+  template <int SET, int J, int M, int N>
   __device__ __forceinline__ void product() {
     if constexpr (!MX) {
       acc[M][N] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
@@ -287,156 +335,213 @@ struct TileProduct {
           __builtin_bit_cast(bf16x8, (i32x4){fb[SET][N][0], fb[SET][N][1], fb[SET][N][2], fb[SET][N][3]}), acc[M][N],
           0, 0, 0);
     } else {
+      constexpr int FB = KB == K_E2M1 ? 4 : 0, Q = J >> 1, OS = 2 * (J & 1);
       const i32x8 x = as_operand<KA>(fa[SET][M]), y = as_operand<KB>(fb[SET][N]);
-      constexpr int FB = KB == K_E2M1 ? 4 : 0;
       if constexpr (SPLIT) {
         i32x8 hi, lo;
         split_e4m3(y, hi, lo);
-        acc[M][N] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, lo, acc[M][N], 4, FB, 2 * J, sca[M][Q], 2 * J,
-                                                                    scb[N][Q]);
-        acc[M][N] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, hi, acc[M][N], 4, FB, 2 * J, sca[M][Q], 2 * J,
-                                                                    scb[N][Q]);
+        acc[M][N] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, lo, acc[M][N], 4, FB, OS, sca[M][Q], OS, scb[N][Q]);
+        acc[M][N] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, hi, acc[M][N], 4, FB, OS, sca[M][Q], OS, scb[N][Q]);
       } else {
-        acc[M][N] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, acc[M][N], 4, FB, 2 * J, sca[M][Q], 2 * J,
-                                                                    scb[N][Q]);
+        acc[M][N] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, acc[M][N], 4, FB, OS, sca[M][Q], OS, scb[N][Q]);
       }
     }
   }
 
-  // transfers in flight that may remain when stage Q (mod 4) + 1 is needed: those of the NSTG - 2 stages after it
-  static constexpr int pending(int q) {
-    int n = 0;
-    for (int s = 2; s < NSTG; ++s) n += PER + ((MX && (q + s) % 4 == 0) ? SC : 0);
-    return n;
-  }
-
-  template <int Q>
-  __device__ __forceinline__ void stage() {
-    if constexpr (MX && Q == 0) {
-      const int sh = 8 * (lane >> 5);  // lanes 32..63 take the odd blocks' bytes
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-#pragma unroll
-        for (int m = 0; m < MB; ++m) sca[m][q] = (int)((uint32_t)nca[m][q] >> sh);
-#pragma unroll
-        for (int n = 0; n < NB; ++n) scb[n][q] = (int)((uint32_t)ncb[n][q] >> sh);
-      }
-    }
-    if constexpr (MX && (Q + NSTG - 1) % 4 == 0) transfer_scales();
-    // first step; between its products the second step's fragments and the transfers of the stage NSTG - 1 ahead
+  // step J; between its products the fragments of the next step (of the stage at `from`) and transfers T0 .. T1 - 1
+  // of the stage being brought into `to`
+  template <int J, int T0, int T1>
+  __device__ __forceinline__ void step(uint32_t from, uint32_t to) {
     static_for<0, NM>([&](auto ic) {
       constexpr int i = decltype(ic)::value;
-      product<0, Q, 0, i / NB, i % NB>();
-      static_for<i * (MB + NB) / NM, (i + 1) * (MB + NB) / NM>([&](auto t) { read_frag<1, 1, decltype(t)::value>(); });
-      static_for<i * PER / NM, (i + 1) * PER / NM>([&](auto t) { transfer(decltype(t)::value); });
-      __builtin_amdgcn_sched_barrier(0);
-    });
-    wait_and_barrier<pending(Q)>();
-    slot_r = next_slot(slot_r);
-    static_for<0, NM>([&](auto ic) {
-      constexpr int i = decltype(ic)::value;
-      product<1, Q, 1, i / NB, i % NB>();
-      static_for<i * (MB + NB) / NM, (i + 1) * (MB + NB) / NM>([&](auto t) {
-        read_frag<0, 0, decltype(t)::value>();
-        if constexpr (MX && Q == 3) read_scale<decltype(t)::value>();
-      });
+      product<J & 1, J, i / NB, i % NB>();
+      static_for<i * (MB + NB) / NM, (i + 1) * (MB + NB) / NM>(
+          [&](auto t) { read_frag<(J + 1) & 1, (J + 1) & 3, decltype(t)::value>(from); });
+      static_for<T0 + i * (T1 - T0) / NM, T0 + (i + 1) * (T1 - T0) / NM>([&](auto t) { transfer(decltype(t)::value, to); });
       __builtin_amdgcn_sched_barrier(0);
     });
   }
 
-  // nk stages; MX operands take them four at a time (512 columns), those past the last one multiplying zeros (the
-  // stretches end there, and the format keeps the scale bytes behind a row's last block at 0)
-  __device__ __forceinline__ void run(int nk) {
-    static_for<0, NSTG - 1>([&](auto s) {
-      if constexpr (MX && decltype(s)::value % 4 == 0) transfer_scales();
-#pragma unroll
-      for (int i = 0; i < PER; ++i) transfer(i);
-    });
-    wait_and_barrier<pending(3)>();
-    static_for<0, MB + NB>([&](auto t) {
-      read_frag<0, 0, decltype(t)::value>();
-      if constexpr (MX) read_scale<decltype(t)::value>();
-    });
+  // stage `at` of nk, the P-th of a pair
+  template <int P>
+  __device__ __forceinline__ void stage(int at, int nk) {
+    const uint32_t other = STAGE - slot;
+    if constexpr (MX) take_scales<P>();
+    step<0, D3, D0>(slot, other);
+    step<1, D0, D1>(slot, other);
+    step<2, D1, D1>(slot, other);
+    wait_and_barrier<0>();
+    const bool cross = at + 2 == nk;  // the next stage to bring is the next tile's first
+    a.mem.take_if(cross, an), b.mem.take_if(cross, bn);
     if constexpr (MX) {
-      for (int kt = 0; kt < nk; kt += 4) stage<0>(), stage<1>(), stage<2>(), stage<3>();
-    } else {
-      for (int kt = 0; kt < nk; ++kt) stage<0>();
+      // Scale bytes are read two stages at a time. Those of the four stages that the buffer holds have all been read
+      // when the third's last step begins (the tile's when its last stage but one's does); the next ones arrive before
+      // the fourth's.
+      if constexpr (P == 1) {
+        read_scales(at + 1 == nk ? 0 : at + 1);
+      } else {
+        Stretch ga = sa.at((at + 2) >> 2), gb = sb.at((at + 2) >> 2);
+        ga.take_if(cross, san), gb.take_if(cross, sbn);
+        transfer_scales(((at & 3) ^ 2) & (cross ? 0 : -1), ga, gb);
+      }
     }
-    wait_and_barrier<0>();  // nothing may still be writing LDS when the workgroup moves on
+    step<3, 0, D3>(other, slot);
+    slot = other;
+  }
+
+  // Brings the first tile's first stages and reads its first fragments. nk >= 2 for every tile, and even for MX
+  // operands: stages past the operands' last one multiply zeros (their transfers bring zeros, and the format keeps the
+  // scale bytes behind a row's last block at 0).
+  __device__ __forceinline__ void start() {
+    if constexpr (MX) transfer_scales(0, sa, sb);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) transfer(i, 0);
+#pragma unroll
+    for (int i = 0; i < D3; ++i) transfer(i, STAGE);
+    wait_and_barrier<D3>();
+    static_for<0, MB + NB>([&](auto t) { read_frag<0, 0, decltype(t)::value>(0); });
+    if constexpr (MX) read_scales(0);
+  }
+
+  // A tile; when it ends, the first stages of the next one (an, bn, san, sbn; no stages if there is none) are on their
+  // way.
+  __device__ __forceinline__ void multiply(int nk) {
+    if constexpr (MX) {
+      for (int at = 0; at < nk; at += 2) stage<0>(at, nk), stage<1>(at + 1, nk);
+      sa = san, sb = sbn;
+    } else {
+      for (int at = 0; at < nk; ++at) stage<0>(at, nk);
+    }
   }
 };
 
-// Tile of workgroup b of `grid` (a multiple of 8, at least `tiles`), false for the grid's surplus. Workgroup b runs on
-// XCD b mod 8: each XCD owns a run of tiles, ordered in strips of up to 8 tiles of the second operand, so that the tiles
-// that run together on an XCD share operands in its L2.
-__device__ __forceinline__ bool tile_of(int b, int grid, int ta, int tb, int& ia, int& ib) {
-  const int p = (b & 7) * (grid >> 3) + (b >> 3);
-  if (p >= ta * tb) return false;
-  const int strip = p / (8 * ta), rest = p - strip * 8 * ta;
-  const int h = min(8, tb - strip * 8);
-  ia = rest / h, ib = strip * 8 + rest % h;
-  return true;
+// Order of the tiles. A launch has up to one workgroup for each place that the chip has for it, a multiple of 8; workgroup
+// b runs on XCD b mod 8. Each XCD owns a run of tiles, ordered in strips of up to 8 tiles of the second operand, and its
+// workgroups take them in turn, so that the tiles that run together on an XCD share operands in its L2.
+struct TileOrder {
+  int per_xcd, start, end, step, ta, tb;
+  __device__ __forceinline__ void init(int b, int grid, int ta_, int tb_) {
+    ta = ta_, tb = tb_, step = grid >> 3;
+    per_xcd = (ta * tb + 7) / 8;
+    start = (b & 7) * per_xcd + (b >> 3);
+    end = min(ta * tb, ((b & 7) + 1) * per_xcd);
+  }
+  // the r-th tile of this workgroup; false: there is none
+  __device__ __forceinline__ bool get(int r, int& ia, int& ib) const {
+    const int p = start + r * step;
+    if (p >= end) return false;
+    const int strip = p / (8 * ta), rest = p - strip * 8 * ta;
+    const int h = min(8, tb - strip * 8);
+    ia = rest / h, ib = strip * 8 + rest % h;
+    return true;
+  }
+};
+
+// workgroups of a launch of `tiles`, `places` fitting the chip at once
+static inline unsigned tile_grid(int64_t tiles, int places) {
+  return (unsigned)(tiles < places ? (tiles + 7) / 8 * 8 : places);
 }
 
-static inline unsigned tile_grid(int64_t tiles) { return (unsigned)((tiles + 7) / 8 * 8); }
-
-// Writes a wave's results, 32 NB rows of Y (from row0 on, of `rows`) by 32 MB columns (from c0 on, of `cols`), through LDS,
-// so that a store takes whole runs of a row: register i of lane l of acc[mb][nb] is row 32 nb + l % 32, column
-// 32 mb + 8 (i / 4) + 4 (l / 32) + i % 4. finish(row, c, v) completes V consecutive results. vec: Y's rows are 16-byte
-// aligned. lds: the workgroup's ring, no longer in use; each wave takes a part of its own.
-template <bool YBF16, int MB, int NB, typename F>
+// Writes a wave's results, 32 NB rows of Y (from row0 on, of `rows`) by 32 MB columns (from c0 on, of `cols`): register i
+// of lane l of acc[mb][nb] is row 32 nb + l % 32, column 32 mb + 8 (i / 4) + 4 (l / 32) + i % 4. They go through LDS, so
+// that a store takes runs of 32 PB columns of a row (16-byte stores straight from the registers, 32 bytes of a row each,
+// took 1.6 times as long for fp32 results of 8192 x 8192 and as long for bf16). vec: Y's rows are 16-byte aligned.
+// lds: 4 PB KB a wave.
+//
+// The code of this part counts: it runs once a tile, and comes from memory if it is long (with the edges' cases expanded
+// for each block it grew to 90 KB, and the 4-bit product at 16384 x 4096 x 11008 took 446 us instead of 390). Blocks
+// inside Y take 16-byte stores, a lane completing V consecutive columns of IT rows: done.columns(c) is called for each
+// new c, done.row(set, it, row, c) for each row of the next block, done.settle(set) before a block's first store and
+// done.finish(set, it, v) to complete its results. Blocks at an edge, or with rows that are not aligned, go one column a lane
+// by done.one(row, c, v).
+template <bool YBF16, int PB, int MB, int NB, typename D>
 __device__ __forceinline__ void store_rows(const f32x16 (&acc)[MB][NB], uint8_t* lds, void* __restrict__ Y, int64_t ld,
-                                           int64_t row0, int64_t rows, int c0, int cols, bool vec, bool add,
-                                           F&& finish) {
-  constexpr int C = 32 * MB, PITCH = C + 4, V = YBF16 ? 8 : 4, PER_ROW = C / V, STEP = 64 / PER_ROW;
+                                           int64_t row0, int64_t rows, int c0, int cols, bool vec, bool add, D&& done) {
+  constexpr int C = 32 * PB, V = YBF16 ? 8 : 4, PER_ROW = C / V, STEP = 64 / PER_ROW, IT = 32 / STEP;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  float* buf = reinterpret_cast<float*>(lds) + wave * (32 * PITCH);
+  float* buf = reinterpret_cast<float*>(lds + wave * (4096 * PB));
   const int r = lane & 31, h = lane >> 5;
-  const int c = c0 + (lane % PER_ROW) * V;
-  const bool whole = vec && c + V <= cols;
+  const bool inside = vec && row0 + 32 * NB <= rows && c0 + 32 * MB <= cols;
+  // the 16-byte chunks of row r are permuted by XOR with r, so that neither side's rows meet on the same banks
+  auto chunk = [](int row, int q) { return row * C + ((q ^ (row & (C / 4 - 1))) << 2); };
+  auto fetch = [&](int b) {  // what block b's rows need, into set b % 2
+    const int64_t first = row0 + b % NB * 32 + lane / PER_ROW;
+    const int c = c0 + 32 * PB * (b / NB) + (lane % PER_ROW) * V;
 #pragma unroll
-  for (int nb = 0; nb < NB; ++nb) {
+    for (int it = 0; it < IT; ++it) done.row(b % 2, it, first + it * STEP, c);
+  };
+  if (inside) fetch(0);
 #pragma unroll
-    for (int mb = 0; mb < MB; ++mb)
+  for (int m0 = 0; m0 < MB; m0 += PB) {
+    const int c = c0 + 32 * m0 + (lane % PER_ROW) * V;
+    if (inside) done.columns(c);
 #pragma unroll
-      for (int g = 0; g < 4; ++g)
-        *reinterpret_cast<float4*>(buf + r * PITCH + mb * 32 + 8 * g + 4 * h) =
-            make_float4(acc[mb][nb][4 * g], acc[mb][nb][4 * g + 1], acc[mb][nb][4 * g + 2], acc[mb][nb][4 * g + 3]);
-    __builtin_amdgcn_wave_barrier();
-#pragma unroll 2
-    for (int i = lane / PER_ROW; i < 32; i += STEP) {
-      const int64_t row = row0 + nb * 32 + i;
-      if (row >= rows || c >= cols) continue;
-      float v[V];
+    for (int nb = 0; nb < NB; ++nb) {
+      const int b = m0 / PB * NB + nb;
+      const int64_t first = row0 + nb * 32 + lane / PER_ROW;
+      if (inside && b + 1 < MB / PB * NB) fetch(b + 1);
 #pragma unroll
-      for (int q = 0; q < V / 4; ++q) {
-        const float4 x = *reinterpret_cast<const float4*>(buf + i * PITCH + c - c0 + 4 * q);
-        v[4 * q] = x.x, v[4 * q + 1] = x.y, v[4 * q + 2] = x.z, v[4 * q + 3] = x.w;
-      }
-      finish(row, c, v);
-      if (YBF16) {
-        uint16_t* p = static_cast<uint16_t*>(Y) + row * ld + c;
-        if (whole) {
-          *reinterpret_cast<uint4*>(p) = make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]),
-                                                    bf16_pair(v[V - 4], v[V - 3]), bf16_pair(v[V - 2], v[V - 1]));
-        } else {
-          for (int q = 0; q < V; ++q)
-            if (c + q < cols) p[q] = (uint16_t)bf16_bits(v[q]);
+      for (int mb = 0; mb < PB; ++mb)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          *reinterpret_cast<float4*>(buf + chunk(r, mb * 8 + 2 * g + h)) =
+              make_float4(acc[m0 + mb][nb][4 * g], acc[m0 + mb][nb][4 * g + 1], acc[m0 + mb][nb][4 * g + 2],
+                          acc[m0 + mb][nb][4 * g + 3]);
+      __builtin_amdgcn_wave_barrier();
+      done.settle(b % 2);
+      if (inside) {
+#pragma unroll
+        for (int it = 0; it < IT; ++it) {
+          float v[V];
+#pragma unroll
+          for (int q = 0; q < V / 4; ++q) {
+            const float4 x = *reinterpret_cast<const float4*>(
+                buf + chunk(lane / PER_ROW + it * STEP, (lane % PER_ROW) * (V / 4) + q));
+            v[4 * q] = x.x, v[4 * q + 1] = x.y, v[4 * q + 2] = x.z, v[4 * q + 3] = x.w;
+          }
+          done.finish(b % 2, it, v);
+          const int64_t at = (first + it * STEP) * ld + c;
+          if (YBF16) {
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(Y) + at) =
+                make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[V - 4], v[V - 3]),
+                           bf16_pair(v[V - 2], v[V - 1]));
+          } else {
+            float4* p = reinterpret_cast<float4*>(static_cast<float*>(Y) + at);
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (add) o = *p;
+            *p = make_float4(o.x + v[0], o.y + v[1], o.z + v[2], o.w + v[3]);
+          }
         }
       } else {
-        float* p = static_cast<float*>(Y) + row * ld + c;
-        if (whole) {
-          float4* p4 = reinterpret_cast<float4*>(p);
-          const float4 o = add ? *p4 : make_float4(0.f, 0.f, 0.f, 0.f);
-          *p4 = add ? make_float4(o.x + v[0], o.y + v[1], o.z + v[2], o.w + v[3]) : make_float4(v[0], v[1], v[2], v[3]);
-        } else {
-          for (int q = 0; q < V; ++q)
-            if (c + q < cols) p[q] = add ? p[q] + v[q] : v[q];
+        const int e = c0 + 32 * m0 + (lane & (C - 1));
+        const int n = (int)max((int64_t)0, min((int64_t)32, rows - (row0 + nb * 32)));
+        if (e < cols) {
+#pragma unroll 1
+          for (int i = lane / C; i < n; i += 64 / C) {
+            const int64_t row = row0 + nb * 32 + i;
+            const float v = done.one(row, e, buf[chunk(i, (lane & (C - 1)) >> 2) + (lane & 3)]);
+            if (YBF16) {
+              static_cast<uint16_t*>(Y)[row * ld + e] = (uint16_t)bf16_bits(v);
+            } else {
+              float* p = static_cast<float*>(Y) + row * ld + e;
+              *p = add ? *p + v : v;
+            }
+          }
         }
       }
+      __builtin_amdgcn_wave_barrier();
     }
-    __builtin_amdgcn_wave_barrier();
   }
 }
+
+// partial products leave as they are
+struct StoreAsIs {
+  __device__ __forceinline__ void columns(int) {}
+  __device__ __forceinline__ void row(int, int, int64_t, int) {}
+  __device__ __forceinline__ void settle(int) {}
+  __device__ __forceinline__ float one(int64_t, int, float v) { return v; }
+  template <int V>
+  __device__ __forceinline__ void finish(int, int, float (&)[V]) {}
+};
 
 }  // namespace gptq
