@@ -159,13 +159,14 @@ void matmul_go(const MatmulPlan& p, dim3 grid, hipStream_t stream, const MatmulA
 }  // namespace
 
 size_t mx_matmul_ws_bytes(int64_t n, int64_t in, int64_t out, int a_fmt) {
-  if (n == 0) return 0;
+  if (n <= MX_FEW) return 0;
   const MatmulPlan p = matmul_plan(n, in, out, a_fmt);
   return p.slices > 1 ? align_up((size_t)p.slices * n * out * 4, 256) : 0;
 }
 
 hipError_t mx_matmul_launch(const MxMatrix& a, const MxMatrix& w, const float* bias, int relu, void* Y, int y_dtype,
                             int64_t ld_y, void* ws, hipStream_t stream) {
+  if (a.rows <= MX_FEW) return mx_matmul_few_launch(a, w, bias, relu, Y, y_dtype, ld_y, stream);
   const MatmulPlan p = matmul_plan(a.rows, a.cols, w.rows, a.fmt);
   const bool bf16 = y_dtype == GPTQ_BF16;
   const int64_t srow = mx_scale_row(a.cols), crow = mx_code_row(a.cols, a.fmt);
@@ -206,6 +207,7 @@ hipError_t mx_matmul_launch(const MxMatrix& a, const MxMatrix& w, const float* b
 }
 
 size_t mx_linear_ws_bytes(int64_t n, int64_t in, int64_t out, int act_fmt) {
+  if (mx_few_fused(n, in)) return 0;
   return align_up(n * mx_code_row(in, act_fmt), 256) + align_up(n * mx_scale_row(in), 256) +
          mx_matmul_ws_bytes(n, in, out, act_fmt);
 }
@@ -213,6 +215,7 @@ size_t mx_linear_ws_bytes(int64_t n, int64_t in, int64_t out, int act_fmt) {
 hipError_t mx_linear_launch(const void* X, int x_dtype, int64_t n, int64_t ld_x, int act_fmt, const MxMatrix& w,
                             const float* bias, int relu, void* Y, int y_dtype, int64_t ld_y, void* ws,
                             hipStream_t stream) {
+  if (mx_few_fused(n, w.cols)) return mx_linear_few_launch(X, x_dtype, n, ld_x, act_fmt, w, bias, relu, Y, y_dtype, ld_y, stream);
   uint8_t* codes = static_cast<uint8_t*>(ws);
   uint8_t* scales = codes + align_up(n * mx_code_row(w.cols, act_fmt), 256);
   uint8_t* rest = scales + align_up(n * mx_scale_row(w.cols), 256);

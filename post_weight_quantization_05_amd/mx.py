@@ -16,12 +16,13 @@ can be captured into a graph.
 from __future__ import annotations
 
 from dataclasses import dataclass
+from functools import lru_cache
 
 import torch
 
 from . import _lib
 from ._lib import GPTQ_BF16, GPTQ_F32, GPTQ_MX_E2M1, GPTQ_MX_E4M3, check
-from .gptq import _dtype_code, _ld, _on, _req_cuda, _stream
+from .gptq import _dtype_code, _ld, _on, _req_cuda, _stream as _stream_handle
 
 __all__ = [
     "MXTensor", "mx_quantize", "mx_dequantize", "mx_matmul", "mx_linear", "mx_grad_input", "mx_grad_weight",
@@ -79,43 +80,65 @@ class MXTensor:
         return MXTensor(self.codes[start:stop], self.scales[start:stop], self.cols, self.fmt)
 
 
-def _mx(t: MXTensor, name: str, device=None, cols: int | None = None, rows: int | None = None) -> int:
-    """Checks an operand's storage; its format code."""
+# A call's kernels may take only a few microseconds, so the ordinary case passes each check once, on integers, and only
+# a failure looks for its reason.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream, device_index: int) -> int:
+    """Handle of `stream`, or of the device's current one."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(device_index)
+    return _stream_handle(stream)
+
+
+def _empty(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with _on(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
+def _mx(t: MXTensor, name: str, device: int | None = None, cols: int | None = None, rows: int | None = None) -> int:
+    """Checks an operand's storage; its format code. device: the index that it has to be on."""
     if not isinstance(t, MXTensor):
         raise TypeError(f"{name} must be an MXTensor")
-    code = _fmt_code(t.fmt)
-    c, s = t.codes, t.scales
+    code = _FMT.get(t.fmt) if isinstance(t.fmt, str) else None
+    c, s, d = t.codes, t.scales, t.cols
+    n = c.shape[0]
+    if (code is not None and c.is_cuda and s.is_cuda and d >= 1 and (cols is None or d == cols)
+            and (rows is None or n == rows) and c.dtype == torch.uint8 and s.dtype == torch.uint8
+            and c.shape == (n, _code_row(d, t.fmt)) and s.shape == (n, _scale_row(d)) and c.is_contiguous()
+            and s.is_contiguous() and c.get_device() == s.get_device()
+            and (device is None or c.get_device() == device)):
+        return code
+    _fmt_code(t.fmt)
     if not (c.is_cuda and s.is_cuda):
         raise ValueError(f"{name} must hold device tensors")
-    if t.cols < 1:
+    if d < 1:
         raise ValueError(f"{name} has no columns")
-    if cols is not None and t.cols != cols:
-        raise ValueError(f"{name} has {t.cols} columns, {cols} expected")
-    n = c.shape[0]
+    if cols is not None and d != cols:
+        raise ValueError(f"{name} has {d} columns, {cols} expected")
     if rows is not None and n != rows:
         raise ValueError(f"{name} has {n} rows, {rows} expected")
-    if (c.dtype != torch.uint8 or s.dtype != torch.uint8 or c.shape != (n, _code_row(t.cols, t.fmt))
-            or s.shape != (n, _scale_row(t.cols)) or not c.is_contiguous() or not s.is_contiguous()):
-        raise ValueError(f"{name} must hold contiguous uint8 codes {(n, _code_row(t.cols, t.fmt))} and scales "
-                         f"{(n, _scale_row(t.cols))}")
-    if s.device != c.device or (device is not None and c.device != device):
-        raise ValueError(f"{name} is on {c.device} and {s.device}, {device or c.device} expected")
-    return code
+    if s.device != c.device or (device is not None and c.get_device() != device):
+        raise ValueError(f"{name} is on {c.device} and {s.device}, device {device} expected")
+    raise ValueError(f"{name} must hold contiguous uint8 codes {(n, _code_row(d, t.fmt))} and scales "
+                     f"{(n, _scale_row(d))}")
 
 
-def _w4(t: MXTensor, name: str, device=None, cols: int | None = None, rows: int | None = None) -> None:
+def _w4(t: MXTensor, name: str, device: int | None = None, cols: int | None = None, rows: int | None = None) -> None:
     if _mx(t, name, device, cols, rows) != GPTQ_MX_E2M1:
         raise ValueError(f"{name} must be an e2m1 MXTensor")
 
 
-def _result(out, name: str, shape, dtype, device, stream) -> torch.Tensor:
+def _result(out, name: str, shape, dtype, like: torch.Tensor, stream):
+    """The result's tensor and its leading dimension."""
     if out is None:
-        with _on(stream):
-            return torch.empty(shape, dtype=dtype, device=device)
-    if not out.is_cuda or out.device != device or out.dtype != dtype or tuple(out.shape) != tuple(shape):
-        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {device}")
-    _row_stride(out, name)
-    return out
+        return _empty(shape, dtype, like, stream), shape[1]
+    if not out.is_cuda or out.device != like.device or out.dtype != dtype or tuple(out.shape) != tuple(shape):
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {like.device}")
+    return out, _row_stride(out, name)
 
 
 def _row_stride(t: torch.Tensor, name: str) -> int:
@@ -138,19 +161,24 @@ def _matrix(t: torch.Tensor, name: str) -> int:
     return _row_stride(t, name)
 
 
-def _workspace(need: int, device, stream):
+def _workspace(need: int, like: torch.Tensor, stream):
     if need == 0:
-        return None, 0
-    with _on(stream):
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        return None, None
+    ws = _empty((need,), torch.uint8, like, stream)
     return ws, ws.data_ptr()
 
 
-def _bias_ptr(bias, out: int, device):
+@lru_cache(maxsize=1024)
+def _need(query: str, *sizes) -> int:
+    return getattr(_lib.load(), query)(*sizes)
+
+
+def _bias_ptr(bias, out: int, like: torch.Tensor):
     if bias is None:
         return None
-    if bias.device != device or bias.dtype != torch.float32 or tuple(bias.shape) != (out,) or not bias.is_contiguous():
-        raise ValueError(f"bias must be a contiguous float32 tensor of shape {(out,)} on {device}")
+    if (bias.device != like.device or bias.dtype != torch.float32 or bias.shape != (out,)
+            or not bias.is_contiguous()):
+        raise ValueError(f"bias must be a contiguous float32 tensor of shape {(out,)} on {like.device}")
     return bias.data_ptr()
 
 
@@ -163,21 +191,20 @@ def mx_quantize(X: torch.Tensor, fmt: str = "e2m1", stream=None) -> MXTensor:
     ld = _matrix(X, "X")
     n, d = X.shape
     xt = _dtype_code(X)
-    with _on(stream):
-        codes = torch.empty((n, _code_row(d, fmt)), dtype=torch.uint8, device=X.device)
-        scales = torch.empty((n, _scale_row(d)), dtype=torch.uint8, device=X.device)
+    codes = _empty((n, _code_row(d, fmt)), torch.uint8, X, stream)
+    scales = _empty((n, _scale_row(d)), torch.uint8, X, stream)
     check(_lib.load().gptq_mx_quantize(X.data_ptr(), xt, n, d, ld, code, codes.data_ptr(), scales.data_ptr(),
-                                       _stream(stream)), "gptq_mx_quantize")
+                                       _stream(stream, X.get_device())), "gptq_mx_quantize")
     return MXTensor(codes, scales, d, fmt)
 
 
 def mx_dequantize(Q: MXTensor, dtype=torch.bfloat16, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The values Q stands for, exactly (bf16 or fp32)."""
     code, yt = _mx(Q, "Q"), _out_code(dtype)
-    dev = Q.codes.device
-    Y = _result(out, "out", Q.shape, dtype, dev, stream)
-    check(_lib.load().gptq_mx_dequantize(Q.codes.data_ptr(), Q.scales.data_ptr(), code, Q.rows, Q.cols, Y.data_ptr(),
-                                         yt, _row_stride(Y, "out"), _stream(stream)), "gptq_mx_dequantize")
+    c, n, d = Q.codes, Q.codes.shape[0], Q.cols
+    Y, ld = _result(out, "out", (n, d), dtype, c, stream)
+    check(_lib.load().gptq_mx_dequantize(c.data_ptr(), Q.scales.data_ptr(), code, n, d, Y.data_ptr(), yt, ld,
+                                         _stream(stream, c.get_device())), "gptq_mx_dequantize")
     return Y
 
 
@@ -185,17 +212,18 @@ def mx_matmul(A: MXTensor, W: MXTensor, bias: torch.Tensor | None = None, relu: 
               out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Y = A W^T (+ bias, then ReLU when asked): A n x in (e2m1 or e4m3), W out x in (e2m1), Y n x out."""
     code = _mx(A, "A")
-    dev = A.codes.device
-    _w4(W, "W", dev, A.cols)
+    c, n, d = A.codes, A.codes.shape[0], A.cols
+    dev = c.get_device()
+    _w4(W, "W", dev, d)
     yt = _out_code(dtype)
-    n, d, no = A.rows, A.cols, W.rows
-    b = _bias_ptr(bias, no, dev)
-    Y = _result(out, "out", (n, no), dtype, dev, stream)
-    lib = _lib.load()
-    ws, wp = _workspace(lib.gptq_mx_matmul_workspace_bytes(n, d, no, code), dev, stream)
-    check(lib.gptq_mx_matmul(A.codes.data_ptr(), A.scales.data_ptr(), code, n, d, W.codes.data_ptr(),
-                             W.scales.data_ptr(), no, b, int(bool(relu)), Y.data_ptr(), yt, _row_stride(Y, "out"), wp,
-                             ws.numel() if ws is not None else 0, _stream(stream)), "gptq_mx_matmul")
+    no = W.codes.shape[0]
+    b = _bias_ptr(bias, no, c)
+    Y, ld = _result(out, "out", (n, no), dtype, c, stream)
+    need = _need("gptq_mx_matmul_workspace_bytes", n, d, no, code)
+    ws, wp = _workspace(need, c, stream)
+    check(_lib.load().gptq_mx_matmul(c.data_ptr(), A.scales.data_ptr(), code, n, d, W.codes.data_ptr(),
+                                     W.scales.data_ptr(), no, b, 1 if relu else 0, Y.data_ptr(), yt, ld, wp, need,
+                                     _stream(stream, dev)), "gptq_mx_matmul")
     return Y
 
 
@@ -204,20 +232,20 @@ def mx_linear(X: torch.Tensor, W: MXTensor, act: str = "e4m3", bias: torch.Tenso
     """Y = Q(X) W^T (+ bias, then ReLU): X (n x in, bf16 or fp32) is quantized to `act` on its way into the product,
     the results being those of mx_quantize and mx_matmul. dtype None: X's."""
     code = _fmt_code(act)
-    ld = _matrix(X, "X")
+    ldx = _matrix(X, "X")
     n, d = X.shape
-    dev = X.device
+    dev = X.get_device()
     _w4(W, "W", dev, d)
     dtype = X.dtype if dtype is None else dtype
     xt, yt = _dtype_code(X), _out_code(dtype)
-    no = W.rows
-    b = _bias_ptr(bias, no, dev)
-    Y = _result(out, "out", (n, no), dtype, dev, stream)
-    lib = _lib.load()
-    ws, wp = _workspace(lib.gptq_mx_linear_workspace_bytes(n, d, no, code), dev, stream)
-    check(lib.gptq_mx_linear(X.data_ptr(), xt, n, d, ld, code, W.codes.data_ptr(), W.scales.data_ptr(), no, b,
-                             int(bool(relu)), Y.data_ptr(), yt, _row_stride(Y, "out"), wp,
-                             ws.numel() if ws is not None else 0, _stream(stream)), "gptq_mx_linear")
+    no = W.codes.shape[0]
+    b = _bias_ptr(bias, no, X)
+    Y, ld = _result(out, "out", (n, no), dtype, X, stream)
+    need = _need("gptq_mx_linear_workspace_bytes", n, d, no, code)
+    ws, wp = _workspace(need, X, stream)
+    check(_lib.load().gptq_mx_linear(X.data_ptr(), xt, n, d, ldx, code, W.codes.data_ptr(), W.scales.data_ptr(), no, b,
+                                     1 if relu else 0, Y.data_ptr(), yt, ld, wp, need, _stream(stream, dev)),
+          "gptq_mx_linear")
     return Y
 
 
@@ -231,20 +259,22 @@ def mx_grad_input(dY: torch.Tensor, W: MXTensor, mask: MXTensor | None = None, d
                   out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """dX = dY W (dY n x out bf16, W out x in e2m1), zero wherever `mask` (n x in, the checkpoint of a ReLU's
     outputs) is not positive."""
-    ld = _grad(dY)
+    ldy = _grad(dY)
     n, no = dY.shape
-    dev = dY.device
+    dev = dY.get_device()
     _w4(W, "W", dev, rows=no)
     d = W.cols
-    mt = _mx(mask, "mask", dev, d, n) if mask is not None else 0
+    mc = ms = None
+    mt = 0
+    if mask is not None:
+        mt = _mx(mask, "mask", dev, d, n)
+        mc, ms = mask.codes.data_ptr(), mask.scales.data_ptr()
     yt = _out_code(dtype)
-    dX = _result(out, "out", (n, d), dtype, dev, stream)
-    lib = _lib.load()
-    ws, wp = _workspace(lib.gptq_mx_grad_input_workspace_bytes(n, d, no), dev, stream)
-    check(lib.gptq_mx_grad_input(dY.data_ptr(), ld, n, no, W.codes.data_ptr(), W.scales.data_ptr(), d,
-                                 mask.codes.data_ptr() if mask is not None else None,
-                                 mask.scales.data_ptr() if mask is not None else None, mt, dX.data_ptr(), yt,
-                                 _row_stride(dX, "out"), wp, ws.numel() if ws is not None else 0, _stream(stream)),
+    dX, ld = _result(out, "out", (n, d), dtype, dY, stream)
+    need = _need("gptq_mx_grad_input_workspace_bytes", n, d, no)
+    ws, wp = _workspace(need, dY, stream)
+    check(_lib.load().gptq_mx_grad_input(dY.data_ptr(), ldy, n, no, W.codes.data_ptr(), W.scales.data_ptr(), d, mc, ms,
+                                         mt, dX.data_ptr(), yt, ld, wp, need, _stream(stream, dev)),
           "gptq_mx_grad_input")
     return dX
 
@@ -254,9 +284,9 @@ def mx_grad_weight(dY: torch.Tensor, A: MXTensor, bias_grad: bool = False, dtype
                    stream=None):
     """dW = dY^T A (dY n x out bf16, A n x in: the checkpoint of the layer's input), and db = dY's column sums in
     fp32 when bias_grad. accumulate adds to `out` (fp32) and `bias_out` instead. Returns (dW, db or None)."""
-    ld = _grad(dY)
+    ldy = _grad(dY)
     n, no = dY.shape
-    dev = dY.device
+    dev = dY.get_device()
     code = _mx(A, "A", dev, rows=n)
     d = A.cols
     wt = _out_code(dtype)
@@ -264,19 +294,14 @@ def mx_grad_weight(dY: torch.Tensor, A: MXTensor, bias_grad: bool = False, dtype
         raise ValueError("accumulate adds to out (and bias_out): pass them")
     if bias_out is not None and not bias_grad:
         raise ValueError("bias_out is given without bias_grad")
-    dW = _result(out, "out", (no, d), dtype, dev, stream)
-    db = None
+    dW, ld = _result(out, "out", (no, d), dtype, dY, stream)
+    db = dbp = None
     if bias_grad:
-        if bias_out is None:
-            with _on(stream):
-                db = torch.empty(no, dtype=torch.float32, device=dev)
-        else:
-            _bias_ptr(bias_out, no, dev)
-            db = bias_out
-    lib = _lib.load()
-    ws, wp = _workspace(lib.gptq_mx_grad_weight_workspace_bytes(n, d, no), dev, stream)
-    check(lib.gptq_mx_grad_weight(dY.data_ptr(), ld, n, no, A.codes.data_ptr(), A.scales.data_ptr(), code, d,
-                                  int(bool(accumulate)), dW.data_ptr(), wt, _row_stride(dW, "out"),
-                                  db.data_ptr() if db is not None else None, wp,
-                                  ws.numel() if ws is not None else 0, _stream(stream)), "gptq_mx_grad_weight")
+        db = _empty((no,), torch.float32, dY, stream) if bias_out is None else bias_out
+        dbp = db.data_ptr() if bias_out is None else _bias_ptr(db, no, dY)
+    need = _need("gptq_mx_grad_weight_workspace_bytes", n, d, no)
+    ws, wp = _workspace(need, dY, stream)
+    check(_lib.load().gptq_mx_grad_weight(dY.data_ptr(), ldy, n, no, A.codes.data_ptr(), A.scales.data_ptr(), code, d,
+                                          1 if accumulate else 0, dW.data_ptr(), wt, ld, dbp, wp, need,
+                                          _stream(stream, dev)), "gptq_mx_grad_weight")
     return dW, db
