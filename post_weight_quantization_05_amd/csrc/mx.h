@@ -59,6 +59,9 @@ hipError_t mx_grad_weight_launch(const uint16_t* dY, int64_t ld_dy, int64_t out,
 typedef __attribute__((ext_vector_type(2))) int i32x2;
 typedef __attribute__((ext_vector_type(4))) int i32x4;
 typedef __attribute__((ext_vector_type(8))) int i32x8;
+// 16 bytes at any address that their elements may have: global memory takes them at full width
+typedef i32x4 __attribute__((aligned(2))) i32x4_any;
+typedef f32x4 __attribute__((aligned(4))) f32x4_any;
 typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
 typedef __attribute__((ext_vector_type(2))) short i16x2;
 typedef __attribute__((ext_vector_type(2))) unsigned short u16x2;

@@ -23,16 +23,18 @@ struct Chunk {
   uint32_t w[XBF16 ? 4 : 8];
 };
 
-template <bool XBF16, bool VEC>
+// columns c .. c + 7 of a row of `in`, zeros behind the last
+template <bool XBF16>
 __device__ __forceinline__ Chunk<XBF16> load_chunk(const void* __restrict__ X, int64_t off, int c, int in) {
   Chunk<XBF16> r;
   constexpr int W = XBF16 ? 4 : 8;
-  if (VEC && c + 8 <= in) {
-    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(X) + off * (XBF16 ? 2 : 4));
+  if (c + 8 <= in) {
+    const i32x4_any* p = reinterpret_cast<const i32x4_any*>(static_cast<const uint8_t*>(X) + off * (XBF16 ? 2 : 4));
 #pragma unroll
     for (int q = 0; q < W / 4; ++q) {
-      const uint4 v = p[q];
-      r.w[4 * q] = v.x, r.w[4 * q + 1] = v.y, r.w[4 * q + 2] = v.z, r.w[4 * q + 3] = v.w;
+      const i32x4 v = p[q];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) r.w[4 * q + e] = (uint32_t)v[e];
     }
   } else if (XBF16) {
     const uint16_t* p = static_cast<const uint16_t*>(X) + off;
@@ -124,6 +126,50 @@ __device__ __forceinline__ void decode8(const uint2 v, float scale, float (&y)[8
     const f32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(v.y, scale, false);
     const f32x2 e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(v.y, scale, true);
     y[0] = a[0], y[1] = a[1], y[2] = b[0], y[3] = b[1], y[4] = d[0], y[5] = d[1], y[6] = e[0], y[7] = e[1];
+  }
+}
+
+// A wave's unit: 512 columns of a row, 64 lanes x 8. unit = row * ks + 512-column segment.
+constexpr int UNIT = 512;
+template <int FMT, bool YBF16>
+__device__ __forceinline__ void dequantize_unit(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
+                                                int in, int ks, int64_t unit, void* __restrict__ Y, int64_t ld) {
+  const int lane = threadIdx.x & 63;
+  const int64_t row = unit / ks;
+  const int seg = (int)(unit - row * ks);
+  const int c = seg * UNIT + lane * 8;
+  if (c >= in) return;
+  const int kp = (in + 127) / 128 * 128;
+  uint2 v = make_uint2(0u, 0u);
+  if (FMT == GPTQ_MX_E2M1) v.x = *reinterpret_cast<const uint32_t*>(codes + row * (kp / 2) + c / 2);
+  else v = *reinterpret_cast<const uint2*>(codes + row * kp + c);
+  const uint32_t byte = scales[row * (ks * 16) + (c >> 5)];
+  float y[8];
+  decode8<FMT>(v, __uint_as_float(byte << 23), y);
+  if (byte == 255u) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) y[q] = __uint_as_float(0x7FC00000u);
+  }
+  if (YBF16) {
+    uint16_t* p = static_cast<uint16_t*>(Y) + row * ld + c;
+    if (c + 8 <= in) {
+      *reinterpret_cast<i32x4_any*>(p) = (i32x4){(int)bf16_pair(y[0], y[1]), (int)bf16_pair(y[2], y[3]),
+                                                 (int)bf16_pair(y[4], y[5]), (int)bf16_pair(y[6], y[7])};
+    } else {
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (c + q < in) p[q] = (uint16_t)bf16_bits(y[q]);
+    }
+  } else {
+    float* p = static_cast<float*>(Y) + row * ld + c;
+    if (c + 8 <= in) {
+      reinterpret_cast<f32x4_any*>(p)[0] = (f32x4){y[0], y[1], y[2], y[3]};
+      reinterpret_cast<f32x4_any*>(p)[1] = (f32x4){y[4], y[5], y[6], y[7]};
+    } else {
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (c + q < in) p[q] = y[q];
+    }
   }
 }
 

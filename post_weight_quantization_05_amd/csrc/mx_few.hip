@@ -103,7 +103,7 @@ __device__ __forceinline__ void few_load(FewPart<SRC>& p, const FewSource<FMT, S
             x.w[4 * k] = v.x, x.w[4 * k + 1] = v.y, x.w[4 * k + 2] = v.z, x.w[4 * k + 3] = v.w;
           }
         } else if (r < a.n && b.col + col < a.in) {
-          x = load_chunk<XBF16, false>(a.X, r * a.ldx + b.col + col, b.col + col, a.in);
+          x = load_chunk<XBF16>(a.X, r * a.ldx + b.col + col, b.col + col, a.in);
         } else {
 #pragma unroll
           for (int k = 0; k < (XBF16 ? 4 : 8); ++k) x.w[k] = 0u;

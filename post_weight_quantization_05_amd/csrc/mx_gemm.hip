@@ -22,7 +22,7 @@ struct MatmulArgs {
   int64_t crow_a, crow_w, srow;  // bytes of a row of codes and of scales
   int out, ta, tb;               // tiles along out and along tokens
   int nk, slice;                 // 128s of columns; those of a slice (a multiple of 4)
-  int relu, vec;
+  int relu;
 };
 
 // bias (may be null) and ReLU
@@ -87,11 +87,11 @@ __global__ __launch_bounds__(256, OCC) void k_mx_matmul(const MatmulArgs g) {
     uint8_t* buf = T::STAYS ? lds + T::LDS - 4 * 4096 * T::PB : lds;
     if (gridDim.y > 1) {
       float* part = static_cast<float*>(g.Y) + blockIdx.y * g.n * (int64_t)g.out;
-      store_rows<false, T::PB>(t.acc, buf, part, g.ld, row0, g.n, c0, g.out, g.vec, false, StoreAsIs());
+      store_rows<false, T::PB>(t.acc, buf, part, g.ld, row0, g.n, c0, g.out, false, StoreAsIs());
     } else {
       StoreLinear<YBF16 ? 8 : 4> done;
       done.bias = g.bias, done.low = g.relu ? 0.f : -__builtin_inff();
-      store_rows<YBF16, T::PB>(t.acc, buf, g.Y, g.ld, row0, g.n, c0, g.out, g.vec, false, done);
+      store_rows<YBF16, T::PB>(t.acc, buf, g.Y, g.ld, row0, g.n, c0, g.out, false, done);
     }
     if (!T::STAYS) return;
     t.clear();
@@ -183,8 +183,7 @@ hipError_t mx_matmul_launch(const MxMatrix& a, const MxMatrix& w, const float* b
     g.ac = a.codes + r * crow, g.as = a.scales + r * srow;
     g.bias = bias, g.relu = relu, g.ld = ld_y;
     g.Y = static_cast<uint8_t*>(Y) + r * ld_y * (bf16 ? 2 : 4);
-    g.vec = vec_rows(g.Y, ld_y, y_dtype);
-    if (slices > 1) g.Y = ws, g.ld = w.rows, g.vec = w.rows % 4 == 0;
+    if (slices > 1) g.Y = ws, g.ld = w.rows;
     const dim3 grid(tile_grid((int64_t)g.ta * g.tb, p.wa == 256 ? 256 : 1 << 30), (unsigned)slices);
     if (a.fmt == GPTQ_MX_E2M1) {
       bf16 ? matmul_go<GPTQ_MX_E2M1, false, true>(p, grid, stream, g)

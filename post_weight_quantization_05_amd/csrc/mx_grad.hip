@@ -6,6 +6,7 @@
 // so that a lane of the result holds four consecutive columns.
 #include <algorithm>
 
+#include "mx_codec.h"
 #include "mx_tile.h"
 
 namespace gptq {
@@ -22,7 +23,10 @@ struct GradArgs {
   int64_t mrow, msrow;
   void* Y;
   int64_t ld;
-  int accumulate, vec;
+  int accumulate;
+  const double* sums;          // column sums' slices, for db
+  int sum_slices;
+  float* db;
 };
 
 // Codes of the mask's 4 consecutive columns from c on (a multiple of 4, below the row's padding)
@@ -88,6 +92,13 @@ template <bool GRAD_INPUT, bool YBF16, int MASK, int WA, int WB, int MB, int NB,
 __global__ __launch_bounds__(256, OCC) void k_mx_grad(const GradArgs g) {
   using T = TileProduct<K_BF16T, GRAD_INPUT ? K_BF16 : K_BF16T, WA, WB, MB, NB, false>;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS];
+  if (!GRAD_INPUT && g.db && blockIdx.y == 0) {
+    for (int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x; c < g.ns; c += (int64_t)gridDim.x * 256) {
+      double sum = g.accumulate ? (double)g.db[c] : 0.0;
+      for (int s = 0; s < g.sum_slices; ++s) sum += g.sums[s * g.ns + c];
+      g.db[c] = (float)sum;
+    }
+  }
   TileOrder order;
   order.init(blockIdx.x, gridDim.x, g.ta, g.tb);
   int ia, ib;
@@ -125,12 +136,12 @@ __global__ __launch_bounds__(256, OCC) void k_mx_grad(const GradArgs g) {
     uint8_t* buf = T::STAYS ? lds + T::LDS - 4 * 4096 * T::PB : lds;
     if (gridDim.y > 1) {
       float* part = static_cast<float*>(g.Y) + blockIdx.y * g.ns * (int64_t)g.nf;
-      store_rows<false, T::PB>(t.acc, buf, part, g.nf, row0, g.ns, c0, g.nf, g.vec, false, StoreAsIs());
+      store_rows<false, T::PB>(t.acc, buf, part, g.nf, row0, g.ns, c0, g.nf, false, StoreAsIs());
     } else {
       constexpr int V = YBF16 ? 8 : 4;
       constexpr int PB = MASK != 0 && !YBF16 ? 1 : T::PB;  // fewer rows at a time where each brings a mask's registers too
       StoreMasked<MASK, V, 16 * PB / V> done = {g, {}, {}};
-      store_rows<YBF16, PB>(t.acc, buf, g.Y, g.ld, row0, g.ns, c0, g.nf, g.vec, g.accumulate, done);
+      store_rows<YBF16, PB>(t.acc, buf, g.Y, g.ld, row0, g.ns, c0, g.nf, g.accumulate, done);
     }
     if (!T::STAYS) return;
     t.clear();
@@ -167,51 +178,75 @@ __global__ __launch_bounds__(256) void k_mx_grad_join(const GradArgs g, const fl
   }
 }
 
-// dY with rows of kp (a multiple of 64) columns, zeros behind the last
-__global__ __launch_bounds__(256) void k_pad_rows(const uint16_t* __restrict__ X, int64_t ld, int64_t n, int cols, int kp,
-                                                  uint16_t* __restrict__ Y) {
-  const int64_t total = n * (kp / 8);
-  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += (int64_t)gridDim.x * 256) {
-    const int64_t row = e / (kp / 8);
-    const int c = (int)(e - row * (kp / 8)) * 8;
-    const uint16_t* p = X + row * ld + c;
-    uint32_t w[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint32_t lo = c + 2 * q < cols ? p[2 * q] : 0u, hi = c + 2 * q + 1 < cols ? p[2 * q + 1] : 0u;
-      w[q] = lo | hi << 16;
+// What both products need first, in one launch: workgroups 0 .. nb_values - 1 write the quantized operand's values in
+// bf16; the next nb_pad copy dY to rows of kp columns, zeros behind the last; the rest add dY's columns in fp64, each 32
+// columns of a slice of rows, eight row groups side by side (the slices are added in their order by the product).
+struct PrepArgs {
+  const uint8_t *codes, *scales;
+  int cols, ks;
+  int64_t units;
+  uint16_t* F;
+  int64_t ldf;
+  const uint16_t* dY;
+  int64_t ld, n;
+  int out, kp;
+  uint16_t* pad;
+  double* sums;
+  int64_t rows;  // of a slice
+  unsigned nb_values, nb_pad, nb_cols;
+};
+
+template <int FMT>
+__global__ __launch_bounds__(256) void k_mx_grad_prep(const PrepArgs a) {
+  unsigned b = blockIdx.x;
+  if (b < a.nb_values) {
+    for (int64_t u = (int64_t)b * 4 + (threadIdx.x >> 6); u < a.units; u += (int64_t)a.nb_values * 4)
+      dequantize_unit<FMT, true>(a.codes, a.scales, a.cols, a.ks, u, a.F, a.ldf);
+    return;
+  }
+  b -= a.nb_values;
+  if (b < a.nb_pad) {
+    const int64_t total = a.n * (a.kp / 8);
+    for (int64_t e = (int64_t)b * 256 + threadIdx.x; e < total; e += (int64_t)a.nb_pad * 256) {
+      const int64_t row = e / (a.kp / 8);
+      const int c = (int)(e - row * (a.kp / 8)) * 8;
+      const Chunk<true> x = load_chunk<true>(a.dY, row * a.ld + c, c, a.out);
+      *reinterpret_cast<uint4*>(a.pad + row * a.kp + c) = make_uint4(x.w[0], x.w[1], x.w[2], x.w[3]);
     }
-    *reinterpret_cast<uint4*>(Y + row * kp + c) = make_uint4(w[0], w[1], w[2], w[3]);
+    return;
+  }
+  b -= a.nb_pad;
+  __shared__ double red[8][32];
+  const int c = (int)(b % a.nb_cols) * 32 + (threadIdx.x & 31), g = threadIdx.x >> 5;
+  const int64_t slice = b / a.nb_cols, r0 = slice * a.rows, r1 = min(a.n, r0 + a.rows);
+  double sum = 0.0;
+  if (c < a.out)
+#pragma unroll 4
+    for (int64_t k = r0 + g; k < r1; k += 8) sum += (double)__uint_as_float((uint32_t)a.dY[k * a.ld + c] << 16);
+  red[g][threadIdx.x & 31] = sum;
+  __syncthreads();
+  if (g == 0 && c < a.out) {
+#pragma unroll
+    for (int q = 1; q < 8; ++q) sum += red[q][threadIdx.x];
+    a.sums[slice * a.out + c] = sum;
   }
 }
 
-// Column sums of dY in fp64: workgroup (x, y) adds 32 columns of a slice of rows, eight row groups side by side; the
-// slices are then added in their order.
-constexpr int SUM_ROWS = 256;
-__global__ __launch_bounds__(256) void k_colsum(const uint16_t* __restrict__ S, int64_t ld, int64_t n, int cols,
-                                                int64_t rows, double* __restrict__ part) {
-  __shared__ double red[8][32];
-  const int c = blockIdx.x * 32 + (threadIdx.x & 31), g = threadIdx.x >> 5;
-  const int64_t r0 = blockIdx.y * rows, r1 = min(n, r0 + rows);
-  double sum = 0.0;
-  if (c < cols)
-#pragma unroll 4
-    for (int64_t k = r0 + g; k < r1; k += 8) sum += (double)__uint_as_float((uint32_t)S[k * ld + c] << 16);
-  red[g][threadIdx.x & 31] = sum;
-  __syncthreads();
-  if (g == 0 && c < cols) {
-#pragma unroll
-    for (int q = 1; q < 8; ++q) sum += red[q][threadIdx.x];
-    part[(int64_t)blockIdx.y * cols + c] = sum;
-  }
-}
-__global__ __launch_bounds__(256) void k_colsum_join(const double* __restrict__ part, int slices, int cols,
-                                                     int accumulate, float* __restrict__ db) {
-  const int c = blockIdx.x * 256 + threadIdx.x;
-  if (c >= cols) return;
-  double sum = accumulate ? (double)db[c] : 0.0;
-  for (int s = 0; s < slices; ++s) sum += part[(int64_t)s * cols + c];
-  db[c] = (float)sum;
+// sums: rows of a slice of the column sums (0: none are wanted)
+hipError_t grad_prep(const MxMatrix& q, uint16_t* F, const uint16_t* dY, int64_t ld, int64_t n, int64_t out, uint16_t* pad,
+                     double* sums, int64_t rows, hipStream_t stream) {
+  PrepArgs a = {};
+  a.codes = q.codes, a.scales = q.scales, a.cols = (int)q.cols, a.ks = (int)ceil_div(q.cols, UNIT);
+  a.units = q.rows * a.ks, a.F = F, a.ldf = ceil_div(q.cols, 128) * 128;
+  a.dY = dY, a.ld = ld, a.n = n, a.out = (int)out, a.kp = (int)ceil_div(out, 128) * 128, a.pad = pad;
+  a.sums = sums, a.rows = rows, a.nb_cols = (unsigned)ceil_div(out, 32);
+  a.nb_values = (unsigned)std::min<int64_t>((int64_t)1 << 20, ceil_div(a.units, 4));
+  a.nb_pad = pad ? (unsigned)std::min<int64_t>(4096, ceil_div(n * (a.kp / 8), 256)) : 0;
+  const unsigned nb_sum = rows ? a.nb_cols * (unsigned)ceil_div(n, rows) : 0;
+  const dim3 grid(a.nb_values + a.nb_pad + nb_sum);
+  if (q.fmt == GPTQ_MX_E2M1) hipLaunchKernelGGL((k_mx_grad_prep<GPTQ_MX_E2M1>), grid, dim3(256), 0, stream, a);
+  else hipLaunchKernelGGL((k_mx_grad_prep<GPTQ_MX_E4M3>), grid, dim3(256), 0, stream, a);
+  return hipGetLastError();
 }
 
 struct GradPlan {
@@ -252,7 +287,7 @@ hipError_t grad_run(const GradPlan& p, GradArgs g, float* part, hipStream_t stre
   const GradArgs fin = g;
   g.slice = p.slice;
   g.ta = (int)ceil_div(g.nf, 64 << p.tile);
-  if (p.slices > 1) g.Y = part, g.ld = g.nf, g.vec = g.nf % 4 == 0;
+  if (p.slices > 1) g.Y = part, g.ld = g.nf;
   g.tb = (int)ceil_div(g.ns, 64 << p.tile);
   grad_go<GI, B, M>(p.tile, dim3(tile_grid((int64_t)g.ta * g.tb, p.tile == 2 ? 256 : 1 << 30), (unsigned)p.slices), stream, g);
   if (p.slices > 1)
@@ -280,25 +315,26 @@ size_t mx_grad_input_ws_bytes(int64_t n, int64_t in, int64_t out) {
 hipError_t mx_grad_input_launch(const uint16_t* dY, int64_t ld_dy, int64_t n, const MxMatrix& w, const MxMatrix* mask,
                                 void* dX, int dx_dtype, int64_t ld_dx, void* ws, hipStream_t stream) {
   const int64_t in = w.cols, out = w.rows, ldf = ceil_div(in, 128) * 128, kp = ceil_div(out, 128) * 128;
-  const hipError_t e = mx_dequantize_launch(w, ws, GPTQ_BF16, ldf, stream);
-  if (e != hipSuccess) return e;
   uint8_t* pad = static_cast<uint8_t*>(ws) + align_up(out * ldf * 2, 256);
   float* part = reinterpret_cast<float*>(pad + align_up(std::min(n, ROWS_MAX) * kp * 2, 256));
   for (int64_t r = 0; r < n; r += ROWS_MAX) {
     GradArgs g = {};
     g.F = static_cast<const uint16_t*>(ws), g.ldf = ldf, g.nk = out;
     g.S = dY + r * ld_dy, g.lds = ld_dy, g.ns = std::min(ROWS_MAX, n - r), g.nf = (int)in;
-    if (!dy_direct(g.S, ld_dy, out, true)) {
-      hipLaunchKernelGGL(k_pad_rows, dim3((unsigned)std::min<int64_t>(4096, ceil_div(g.ns * (kp / 8), 256))), dim3(256), 0,
-                         stream, g.S, ld_dy, g.ns, (int)out, (int)kp, reinterpret_cast<uint16_t*>(pad));
-      g.S = reinterpret_cast<const uint16_t*>(pad), g.lds = kp;
+    const bool direct = dy_direct(g.S, ld_dy, out, true);
+    MxMatrix q = w;
+    if (r > 0) q.rows = 0;  // its values are there
+    if (r == 0 || !direct) {
+      const hipError_t e = grad_prep(q, static_cast<uint16_t*>(ws), g.S, ld_dy, g.ns, out,
+                                     direct ? nullptr : reinterpret_cast<uint16_t*>(pad), nullptr, 0, stream);
+      if (e != hipSuccess) return e;
     }
+    if (!direct) g.S = reinterpret_cast<const uint16_t*>(pad), g.lds = kp;
     if (mask) {
       g.mrow = mx_code_row(in, mask->fmt), g.msrow = mx_scale_row(in);
       g.mc = mask->codes + r * g.mrow, g.ms = mask->scales + r * g.msrow;
     }
     g.Y = static_cast<uint8_t*>(dX) + r * ld_dx * (dx_dtype == GPTQ_BF16 ? 2 : 4), g.ld = ld_dx;
-    g.vec = vec_rows(g.Y, ld_dx, dx_dtype);
     // the plan of the first (largest) piece: its partial products fit the workspace
     const GradPlan p = grad_plan(std::min(n, ROWS_MAX), in, out);
     const int kind = !mask ? 0 : mask->fmt == GPTQ_MX_E2M1 ? 1 : 2;
@@ -317,7 +353,7 @@ hipError_t mx_grad_input_launch(const uint16_t* dY, int64_t ld_dy, int64_t n, co
 namespace {
 int64_t colsum_rows(int64_t n, int64_t out) {
   const int64_t want = std::max<int64_t>(1, 2048 / ceil_div(out, 32));  // about 2048 workgroups
-  return std::max<int64_t>(SUM_ROWS, ceil_div(n, std::min<int64_t>(want, 1024)));
+  return std::max<int64_t>(256, ceil_div(n, std::min<int64_t>(want, 1024)));
 }
 }  // namespace
 
@@ -336,29 +372,18 @@ hipError_t mx_grad_weight_launch(const uint16_t* dY, int64_t ld_dy, int64_t out,
   GradArgs g = {};
   g.F = static_cast<const uint16_t*>(ws), g.ldf = ldf, g.nk = n, g.nf = (int)in;
   g.S = dY, g.lds = ld_dy, g.ns = out, g.Y = dW, g.ld = ld_dw, g.accumulate = accumulate;
-  g.vec = vec_rows(dW, ld_dw, dw_dtype);
+  const int64_t rows = colsum_rows(n, out);
   if (n > 0) {
-    const hipError_t e = mx_dequantize_launch(a, ws, GPTQ_BF16, ldf, stream);
+    const bool direct = dy_direct(dY, ld_dy, out, false);
+    const hipError_t e = grad_prep(a, static_cast<uint16_t*>(ws), dY, ld_dy, n, out,
+                                   direct ? nullptr : reinterpret_cast<uint16_t*>(pad), sums, db ? rows : 0, stream);
     if (e != hipSuccess) return e;
-    if (!dy_direct(dY, ld_dy, out, false)) {
-      hipLaunchKernelGGL(k_pad_rows, dim3((unsigned)std::min<int64_t>(4096, ceil_div(n * (kp / 8), 256))), dim3(256), 0,
-                         stream, dY, ld_dy, n, (int)out, (int)kp, reinterpret_cast<uint16_t*>(pad));
-      g.S = reinterpret_cast<const uint16_t*>(pad), g.lds = kp;
-    }
+    if (!direct) g.S = reinterpret_cast<const uint16_t*>(pad), g.lds = kp;
   }
+  g.db = db, g.sums = sums, g.sum_slices = (int)ceil_div(n, rows);
   const hipError_t s = dw_dtype == GPTQ_BF16 ? grad_run<false, true, 0>(p, g, reinterpret_cast<float*>(part), stream)
                                              : grad_run<false, false, 0>(p, g, reinterpret_cast<float*>(part), stream);
-  if (s != hipSuccess) return s;
-  if (db) {
-    const int64_t rows = colsum_rows(n, out);
-    const int slices = (int)ceil_div(n, rows);
-    if (slices)
-      hipLaunchKernelGGL(k_colsum, dim3((unsigned)ceil_div(out, 32), (unsigned)slices), dim3(256), 0, stream, dY, ld_dy, n,
-                         (int)out, rows, sums);
-    hipLaunchKernelGGL(k_colsum_join, dim3((unsigned)ceil_div(out, 256)), dim3(256), 0, stream, sums, slices, (int)out,
-                       accumulate, db);
-  }
-  return hipGetLastError();
+  return s;
 }
 
 }  // namespace gptq

@@ -12,15 +12,13 @@ namespace gptq {
 
 namespace {
 
-constexpr int UNIT = 512;  // columns per wave and unit: 64 lanes x 8
-
 __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
   v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true));  // lanes 1 0 3 2
   v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true));  // lanes 2 3 0 1
   return v;
 }
 
-template <int FMT, bool XBF16, bool VEC>
+template <int FMT, bool XBF16>
 __global__ __launch_bounds__(256) void k_mx_quantize(const void* __restrict__ X, int64_t ld, int in, int ks,
                                                      int64_t units, uint8_t* __restrict__ codes,
                                                      uint8_t* __restrict__ scales) {
@@ -30,7 +28,7 @@ __global__ __launch_bounds__(256) void k_mx_quantize(const void* __restrict__ X,
   const int64_t row = unit / ks;
   const int seg = (int)(unit - row * ks);
   const int c = seg * UNIT + lane * 8;
-  const Chunk<XBF16> x = load_chunk<XBF16, VEC>(X, row * ld + c, c, in);
+  const Chunk<XBF16> x = load_chunk<XBF16>(X, row * ld + c, c, in);
   const uint32_t byte = scale_byte<FMT>(quad_max(max_bits<XBF16>(chunk_max<XBF16>(x))));
   const int kp = (in + 127) / 128 * 128;
   const float scale = __uint_as_float(byte << 23);
@@ -46,69 +44,12 @@ __global__ __launch_bounds__(256) void k_mx_quantize(const void* __restrict__ X,
   if ((lane & 3) == 0) scales[row * (ks * 16) + (c >> 5)] = (uint8_t)(c < in ? byte : 0u);
 }
 
-template <int FMT, bool YBF16, bool VEC>
+template <int FMT, bool YBF16>
 __global__ __launch_bounds__(256) void k_mx_dequantize(const uint8_t* __restrict__ codes,
                                                        const uint8_t* __restrict__ scales, int in, int ks,
                                                        int64_t units, void* __restrict__ Y, int64_t ld) {
-  const int lane = threadIdx.x & 63;
   const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (unit >= units) return;
-  const int64_t row = unit / ks;
-  const int seg = (int)(unit - row * ks);
-  const int c = seg * UNIT + lane * 8;
-  if (c >= in) return;
-  const int kp = (in + 127) / 128 * 128;
-  uint2 v = make_uint2(0u, 0u);
-  if (FMT == GPTQ_MX_E2M1) v.x = *reinterpret_cast<const uint32_t*>(codes + row * (kp / 2) + c / 2);
-  else v = *reinterpret_cast<const uint2*>(codes + row * kp + c);
-  const uint32_t byte = scales[row * (ks * 16) + (c >> 5)];
-  float y[8];
-  decode8<FMT>(v, __uint_as_float(byte << 23), y);
-  if (byte == 255u) {
-#pragma unroll
-    for (int q = 0; q < 8; ++q) y[q] = __uint_as_float(0x7FC00000u);
-  }
-  if (YBF16) {
-    uint16_t* p = static_cast<uint16_t*>(Y) + row * ld + c;
-    if (VEC && c + 8 <= in) {
-      *reinterpret_cast<uint4*>(p) = make_uint4(bf16_pair(y[0], y[1]), bf16_pair(y[2], y[3]), bf16_pair(y[4], y[5]),
-                                                bf16_pair(y[6], y[7]));
-    } else {
-#pragma unroll
-      for (int q = 0; q < 8; ++q)
-        if (c + q < in) p[q] = (uint16_t)bf16_bits(y[q]);
-    }
-  } else {
-    float* p = static_cast<float*>(Y) + row * ld + c;
-    if (VEC && c + 8 <= in) {
-      reinterpret_cast<float4*>(p)[0] = make_float4(y[0], y[1], y[2], y[3]);
-      reinterpret_cast<float4*>(p)[1] = make_float4(y[4], y[5], y[6], y[7]);
-    } else {
-#pragma unroll
-      for (int q = 0; q < 8; ++q)
-        if (c + q < in) p[q] = y[q];
-    }
-  }
-}
-
-template <int FMT, bool B>
-void quantize_go(bool vec, unsigned grid, hipStream_t stream, const void* X, int64_t ld, int in, int ks, int64_t units,
-                 uint8_t* codes, uint8_t* scales) {
-  if (vec)
-    hipLaunchKernelGGL((k_mx_quantize<FMT, B, true>), dim3(grid), dim3(256), 0, stream, X, ld, in, ks, units, codes, scales);
-  else
-    hipLaunchKernelGGL((k_mx_quantize<FMT, B, false>), dim3(grid), dim3(256), 0, stream, X, ld, in, ks, units, codes, scales);
-}
-
-template <int FMT, bool B>
-void dequantize_go(bool vec, unsigned grid, hipStream_t stream, const MxMatrix& q, int ks, int64_t units, void* Y,
-                   int64_t ld) {
-  if (vec)
-    hipLaunchKernelGGL((k_mx_dequantize<FMT, B, true>), dim3(grid), dim3(256), 0, stream, q.codes, q.scales, (int)q.cols,
-                       ks, units, Y, ld);
-  else
-    hipLaunchKernelGGL((k_mx_dequantize<FMT, B, false>), dim3(grid), dim3(256), 0, stream, q.codes, q.scales,
-                       (int)q.cols, ks, units, Y, ld);
+  if (unit < units) dequantize_unit<FMT, YBF16>(codes, scales, in, ks, unit, Y, ld);
 }
 
 // A launch holds at most this many rows x segments, so that its grid stays below 2^32 work-items.
@@ -119,26 +60,23 @@ constexpr int64_t MAX_UNITS = (int64_t)1 << 25;
 hipError_t mx_quantize_launch(const void* X, int x_dtype, int64_t n, int64_t in, int64_t ld_x, int fmt, uint8_t* codes,
                               uint8_t* scales, hipStream_t stream) {
   const int ks = (int)ceil_div(in, UNIT);
-  const bool vec = vec_rows(X, ld_x, x_dtype), b = x_dtype == GPTQ_BF16;
+  const bool b = x_dtype == GPTQ_BF16;
   const int64_t rows_max = MAX_UNITS / ks;
   for (int64_t r = 0; r < n; r += rows_max) {
     const int64_t units = std::min(rows_max, n - r) * ks;
     const unsigned grid = (unsigned)ceil_div(units, 4);
     const void* x = static_cast<const uint8_t*>(X) + r * ld_x * (b ? 2 : 4);
     uint8_t *c = codes + r * mx_code_row(in, fmt), *s = scales + r * mx_scale_row(in);
-    if (fmt == GPTQ_MX_E2M1)
-      b ? quantize_go<GPTQ_MX_E2M1, true>(vec, grid, stream, x, ld_x, (int)in, ks, units, c, s)
-        : quantize_go<GPTQ_MX_E2M1, false>(vec, grid, stream, x, ld_x, (int)in, ks, units, c, s);
-    else
-      b ? quantize_go<GPTQ_MX_E4M3, true>(vec, grid, stream, x, ld_x, (int)in, ks, units, c, s)
-        : quantize_go<GPTQ_MX_E4M3, false>(vec, grid, stream, x, ld_x, (int)in, ks, units, c, s);
+    const auto kernel = fmt == GPTQ_MX_E2M1 ? (b ? k_mx_quantize<GPTQ_MX_E2M1, true> : k_mx_quantize<GPTQ_MX_E2M1, false>)
+                                            : (b ? k_mx_quantize<GPTQ_MX_E4M3, true> : k_mx_quantize<GPTQ_MX_E4M3, false>);
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(256), 0, stream, x, ld_x, (int)in, ks, units, c, s);
   }
   return hipGetLastError();
 }
 
 hipError_t mx_dequantize_launch(const MxMatrix& q, void* Y, int y_dtype, int64_t ld_y, hipStream_t stream) {
   const int ks = (int)ceil_div(q.cols, UNIT);
-  const bool vec = vec_rows(Y, ld_y, y_dtype), b = y_dtype == GPTQ_BF16;
+  const bool b = y_dtype == GPTQ_BF16;
   const int64_t rows_max = MAX_UNITS / ks;
   for (int64_t r = 0; r < q.rows; r += rows_max) {
     MxMatrix p = q;
@@ -148,12 +86,10 @@ hipError_t mx_dequantize_launch(const MxMatrix& q, void* Y, int y_dtype, int64_t
     void* y = static_cast<uint8_t*>(Y) + r * ld_y * (b ? 2 : 4);
     const int64_t units = p.rows * ks;
     const unsigned grid = (unsigned)ceil_div(units, 4);
-    if (q.fmt == GPTQ_MX_E2M1)
-      b ? dequantize_go<GPTQ_MX_E2M1, true>(vec, grid, stream, p, ks, units, y, ld_y)
-        : dequantize_go<GPTQ_MX_E2M1, false>(vec, grid, stream, p, ks, units, y, ld_y);
-    else
-      b ? dequantize_go<GPTQ_MX_E4M3, true>(vec, grid, stream, p, ks, units, y, ld_y)
-        : dequantize_go<GPTQ_MX_E4M3, false>(vec, grid, stream, p, ks, units, y, ld_y);
+    const auto kernel = q.fmt == GPTQ_MX_E2M1
+                            ? (b ? k_mx_dequantize<GPTQ_MX_E2M1, true> : k_mx_dequantize<GPTQ_MX_E2M1, false>)
+                            : (b ? k_mx_dequantize<GPTQ_MX_E4M3, true> : k_mx_dequantize<GPTQ_MX_E4M3, false>);
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(256), 0, stream, p.codes, p.scales, (int)p.cols, ks, units, y, ld_y);
   }
   return hipGetLastError();
 }

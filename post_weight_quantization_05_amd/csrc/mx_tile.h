@@ -429,23 +429,22 @@ static inline unsigned tile_grid(int64_t tiles, int places) {
 // Writes a wave's results, 32 NB rows of Y (from row0 on, of `rows`) by 32 MB columns (from c0 on, of `cols`): register i
 // of lane l of acc[mb][nb] is row 32 nb + l % 32, column 32 mb + 8 (i / 4) + 4 (l / 32) + i % 4. They go through LDS, so
 // that a store takes runs of 32 PB columns of a row (16-byte stores straight from the registers, 32 bytes of a row each,
-// took 1.6 times as long for fp32 results of 8192 x 8192 and as long for bf16). vec: Y's rows are 16-byte aligned.
-// lds: 4 PB KB a wave.
+// took 1.6 times as long for fp32 results of 8192 x 8192 and as long for bf16). lds: 4 PB KB a wave.
 //
 // The code of this part counts: it runs once a tile, and comes from memory if it is long (with the edges' cases expanded
 // for each block it grew to 90 KB, and the 4-bit product at 16384 x 4096 x 11008 took 446 us instead of 390). Blocks
 // inside Y take 16-byte stores, a lane completing V consecutive columns of IT rows: done.columns(c) is called for each
 // new c, done.row(set, it, row, c) for each row of the next block, done.settle(set) before a block's first store and
-// done.finish(set, it, v) to complete its results. Blocks at an edge, or with rows that are not aligned, go one column a lane
+// done.finish(set, it, v) to complete its results. Blocks at an edge go one column a lane
 // by done.one(row, c, v).
 template <bool YBF16, int PB, int MB, int NB, typename D>
 __device__ __forceinline__ void store_rows(const f32x16 (&acc)[MB][NB], uint8_t* lds, void* __restrict__ Y, int64_t ld,
-                                           int64_t row0, int64_t rows, int c0, int cols, bool vec, bool add, D&& done) {
+                                           int64_t row0, int64_t rows, int c0, int cols, bool add, D&& done) {
   constexpr int C = 32 * PB, V = YBF16 ? 8 : 4, PER_ROW = C / V, STEP = 64 / PER_ROW, IT = 32 / STEP;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   float* buf = reinterpret_cast<float*>(lds + wave * (4096 * PB));
   const int r = lane & 31, h = lane >> 5;
-  const bool inside = vec && row0 + 32 * NB <= rows && c0 + 32 * MB <= cols;
+  const bool inside = row0 + 32 * NB <= rows && c0 + 32 * MB <= cols;
   // the 16-byte chunks of row r are permuted by XOR with r, so that neither side's rows meet on the same banks
   auto chunk = [](int row, int q) { return row * C + ((q ^ (row & (C / 4 - 1))) << 2); };
   auto fetch = [&](int b) {  // what block b's rows need, into set b % 2
@@ -486,14 +485,14 @@ __device__ __forceinline__ void store_rows(const f32x16 (&acc)[MB][NB], uint8_t*
           done.finish(b % 2, it, v);
           const int64_t at = (first + it * STEP) * ld + c;
           if (YBF16) {
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(Y) + at) =
-                make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[V - 4], v[V - 3]),
-                           bf16_pair(v[V - 2], v[V - 1]));
+            *reinterpret_cast<i32x4_any*>(static_cast<uint16_t*>(Y) + at) =
+                (i32x4){(int)bf16_pair(v[0], v[1]), (int)bf16_pair(v[2], v[3]), (int)bf16_pair(v[V - 4], v[V - 3]),
+                        (int)bf16_pair(v[V - 2], v[V - 1])};
           } else {
-            float4* p = reinterpret_cast<float4*>(static_cast<float*>(Y) + at);
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            f32x4_any* p = reinterpret_cast<f32x4_any*>(static_cast<float*>(Y) + at);
+            f32x4 o = {0.f, 0.f, 0.f, 0.f};
             if (add) o = *p;
-            *p = make_float4(o.x + v[0], o.y + v[1], o.z + v[2], o.w + v[3]);
+            *p = o + (f32x4){v[0], v[1], v[2], v[3]};
           }
         }
       } else {
