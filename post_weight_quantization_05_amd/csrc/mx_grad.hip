@@ -258,10 +258,15 @@ struct GradPlan {
 GradPlan grad_plan(int64_t ns, int64_t nf, int64_t nk) {
   GradPlan p = {0, 1, std::max<int64_t>(64, (int64_t)align_up(nk, 64))};
   auto tiles = [&](int64_t w) { return ceil_div(ns, w) * ceil_div(nf, w); };
-  p.tile = tiles(256) >= 192 ? 2 : tiles(128) >= 192 ? 1 : 0;
-  const int64_t t = tiles(64 << p.tile);
-  if (t > 0 && t < 192) {
-    const int64_t s = std::max<int64_t>(1, std::min<int64_t>({512 / t, ceil_div(nk, 256), 64}));
+  // us with tiles of 64 / 128 / 256 (dX): 512 x 4096 x 4096 48 / 54 / 96, 1024 x 4096 x 4096 66 / 58 / 100,
+  // 2048 x 4096 x 4096 109 / 75 / 91, 4096 x 4096 x 4096 200 / 131 / 114, 1500 x 2000 x 3000 (192 tiles of 128) 42 / 50 / -
+  p.tile = tiles(256) >= 192 ? 2 : tiles(128) >= 224 ? 1 : 0;
+  // Slices of k, joined by another launch, where the tiles leave places of the chip empty (three 64 x 64 tiles fit a CU)
+  // and each slice has a long sum: 200 x 4096 x 4096 takes 37 us with 4 and 47 with one, dW 4096 x 1024 x 1024 36 and 44,
+  // but 512 x 1024 x 1024 15.5 with two and 14.0 with one.
+  const int64_t t = tiles(64 << p.tile), places = p.tile == 0 ? 768 : p.tile == 1 ? 512 : 256;
+  if (t > 0) {
+    const int64_t s = std::max<int64_t>(1, std::min<int64_t>({places / t, nk / 1024, 64}));
     p.slice = std::max<int64_t>(64, (int64_t)align_up(ceil_div(nk, s), 64));
   }
   p.slices = (int)std::max<int64_t>(1, ceil_div(nk, p.slice));
