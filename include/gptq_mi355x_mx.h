@@ -42,8 +42,7 @@ typedef enum { GPTQ_MX_E2M1 = 0, GPTQ_MX_E4M3 = 1 } gptq_mx_format;
 int64_t gptq_mx_code_bytes_per_row(int64_t cols, int fmt);
 int64_t gptq_mx_scale_bytes_per_row(int64_t cols);
 
-/* X (n x in, ld_x >= in, GPTQ_F32 or GPTQ_BF16) -> codes and scales. 16-byte aligned rows take the fast load
- * path. */
+/* X (n x in, ld_x >= in, GPTQ_F32 or GPTQ_BF16) -> codes and scales. */
 int gptq_mx_quantize(const void* X, int x_dtype, int64_t n, int64_t in, int64_t ld_x, int fmt, uint8_t* codes,
                      uint8_t* scales, void* stream);
 
@@ -61,7 +60,7 @@ int gptq_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int a_fmt, i
                    void* Y, int y_dtype, int64_t ld_y, void* ws, size_t ws_bytes, void* stream);
 
 /* Y = Q(X) W^T (+ bias) (ReLU): gptq_mx_quantize of X to act_fmt followed by gptq_mx_matmul, in one launch for few
- * tokens. X n x in in x_dtype, ld_x >= in. */
+ * tokens (n <= 16, n x in <= 32768). X n x in in x_dtype, ld_x >= in. */
 size_t gptq_mx_linear_workspace_bytes(int64_t n, int64_t in, int64_t out, int act_fmt);
 int gptq_mx_linear(const void* X, int x_dtype, int64_t n, int64_t in, int64_t ld_x, int act_fmt,
                    const uint8_t* w_codes, const uint8_t* w_scales, int64_t out, const float* bias, int relu,
