@@ -216,7 +216,7 @@ struct TileProduct {
   // Share of a stage's transfers issued by the end of the last step of the stage two before it, then of the next one's first
   // and second. All of them between the last step's products saturate the L1's 64 bytes a cycle while the matrix cores
   // wait (16384 x 4096 x 11008 in 4 bits: 478 us, against 444); spread over all four steps the last ones arrive late (455).
-  static constexpr int D3 = PER * 6 / 16, D0 = PER * 11 / 16, D1 = PER;
+  static constexpr int D3 = PER * 8 / 16, D0 = PER * 12 / 16, D1 = PER;
   static_assert(!MX || (WA % 64 == 0 && WB % 64 == 0), "scale transfers");
 
   A a;
@@ -400,9 +400,11 @@ struct TileProduct {
 };
 
 // Order of the tiles. A launch has up to one workgroup for each place that the chip has for it, a multiple of 8; workgroup
-// b runs on XCD b mod 8. Each XCD owns a run of tiles, ordered in strips of up to 8 tiles of the second operand, and its
-// workgroups take them in turn, so that the tiles that run together on an XCD share operands in its L2.
+// b runs on XCD b mod 8. Each XCD owns a run of tiles, ordered in strips of up to 4 tiles of the second operand, and its
+// workgroups take them in turn, so that the tiles that run together on an XCD share operands in its L2 (of strips of 4 / 8
+// / 16: 16384 x 4096 x 11008 in 4 bits 406 / 407 / 418 us, dW 8192 x 11008 x 4096 628 / 642 / 662).
 struct TileOrder {
+  static constexpr int STRIP = 4;
   int per_xcd, start, end, step, ta, tb;
   __device__ __forceinline__ void init(int b, int grid, int ta_, int tb_) {
     ta = ta_, tb = tb_, step = grid >> 3;
@@ -414,9 +416,9 @@ struct TileOrder {
   __device__ __forceinline__ bool get(int r, int& ia, int& ib) const {
     const int p = start + r * step;
     if (p >= end) return false;
-    const int strip = p / (8 * ta), rest = p - strip * 8 * ta;
-    const int h = min(8, tb - strip * 8);
-    ia = rest / h, ib = strip * 8 + rest % h;
+    const int strip = p / (STRIP * ta), rest = p - strip * STRIP * ta;
+    const int h = min(STRIP, tb - strip * STRIP);
+    ia = rest / h, ib = strip * STRIP + rest % h;
     return true;
   }
 };
