@@ -40,7 +40,7 @@ struct StoreLinear {
     }
   }
   __device__ __forceinline__ void row(int, int, int64_t, int) {}
-  __device__ __forceinline__ void settle(int) {}
+  __device__ __forceinline__ void keep(int, int) {}
   __device__ __forceinline__ void finish(int, int, float (&v)[V]) {
 #pragma unroll
     for (int q = 0; q < V; ++q) v[q] = relu(v[q] + b[q]);
@@ -128,10 +128,11 @@ MatmulPlan matmul_plan(int64_t n, int64_t in, int64_t out, int fmt) {
   const int64_t nk = ceil_div(in, 128);
   auto tiles = [&](int64_t a, int64_t b) { return ceil_div(out, a) * ceil_div(n, b); };
   // The largest tile that gives (nearly) every CU one. us with tiles of 64 / 128 / 256 (E2M1): 512 x 4096 x 4096 13.1 /
-  // 13.8 / 26, 1024 x 4096 x 4096 21.3 / 16.9 / 32, 2048 x 4096 x 4096 37 / 26 / 35, 4096 x 4096 x 4096 67 / 47 / 42.
+  // 13.8 / 26, 1024 x 4096 x 4096 21.3 / 16.9 / 32, 2048 x 4096 x 4096 37 / 26 / 35, 4096 x 4096 x 4096 67 / 47 / 42; with a
+  // short k the results' way out counts more than the products: 8000 x 1024 x 8000 92 / 64 / 74 (E4M3 118 / 100 / 83).
   MatmulPlan p = {64, 64, 1};
   if (fmt == GPTQ_MX_E2M1) {
-    if (tiles(256, 256) >= 256) p = {256, 256, 1};
+    if (tiles(256, 256) >= 256 && nk >= 16) p = {256, 256, 1};
     else if (tiles(128, 128) >= 224) p = {128, 128, 1};
   } else {
     if (tiles(256, 128) >= 256) p = {256, 128, 1};

@@ -52,37 +52,51 @@ __device__ __forceinline__ float masked(const GradArgs& g, int64_t row, int c, f
   }
   return v;
 }
-template <int MASK, int V, int IT>
+template <int MASK, int V, int IT, int BLOCKS>
 struct StoreMasked {
+  static constexpr int J = V / 4;  // groups of four columns of a row; IT J of them fill a word of flags
+  static_assert(IT * J <= 8, "a word of flags a block");
   const GradArgs& g;
-  uint32_t codes[2][IT][V / 4], scale[2][IT];
+  uint32_t codes[4][IT][J], scale[4][IT], flags[BLOCKS];
   __device__ __forceinline__ void columns(int) {}
   __device__ __forceinline__ void row(int set, int it, int64_t row, int c) {
     if constexpr (MASK != 0) {
       scale[set][it] = g.ms[row * g.msrow + (c >> 5)];
 #pragma unroll
-      for (int p = 0; p < V; p += 4) codes[set][it][p / 4] = mask_codes<MASK>(g, row, c + p);
+      for (int p = 0; p < J; ++p) codes[set][it][p] = mask_codes<MASK>(g, row, c + 4 * p);
     }
   }
-  // The loads end here whatever path follows: one left in flight would make the compiler wait for all transfers in the
-  // next tile's loop.
-  __device__ __forceinline__ void settle(int set) {
+  // Four codes at once: the top bit of each is set in `open` where the value is > 0 and a number. Group j's flags lie j
+  // places further down, E2M1's groups 4 to 7 in the upper half.
+  __device__ __forceinline__ void keep(int set, int b) {
     if constexpr (MASK != 0) {
+      uint32_t f = 0;
 #pragma unroll
-      for (int it = 0; it < IT; ++it) {
-        asm volatile("" : "+v"(scale[set][it]));
+      for (int it = 0; it < IT; ++it)
 #pragma unroll
-        for (int p = 0; p < V / 4; ++p) asm volatile("" : "+v"(codes[set][it][p]));
-      }
+        for (int p = 0; p < J; ++p) {
+          const uint32_t w = codes[set][it][p];
+          const int j = it * J + p;
+          uint32_t open;
+          if (MASK == 1) {
+            open = ((w & 0x7777u) + 0x7777u) & ~w & 0x8888u;
+          } else {
+            const uint32_t m = w & 0x7F7F7F7Fu;
+            open = (m + 0x7F7F7F7Fu) & ~(m + 0x01010101u) & ~w & 0x80808080u;
+          }
+          open = scale[set][it] == 255u ? 0u : open;
+          f |= MASK == 1 ? open >> (3 - (j & 3)) << (16 * (j >> 2)) : open >> (7 - j);
+        }
+      flags[b] = f;
     }
   }
   __device__ __forceinline__ float one(int64_t row, int c, float v) { return masked<MASK>(g, row, c, v); }
-  __device__ __forceinline__ void finish(int set, int it, float (&v)[V]) {
+  __device__ __forceinline__ void finish(int b, int it, float (&v)[V]) {
     if constexpr (MASK != 0) {
 #pragma unroll
       for (int q = 0; q < V; ++q) {
-        const uint32_t k = scale[set][it] == 255 ? 0u : codes[set][it][q >> 2];
-        if (!mask_open<MASK>(k, q & 3)) v[q] = 0.f;
+        const int j = it * J + (q >> 2), at = MASK == 1 ? 4 * (q & 3) + (j & 3) + 16 * (j >> 2) : 8 * (q & 3) + j;
+        v[q] = __uint_as_float(__float_as_uint(v[q]) & (uint32_t)((int)(flags[b] << (31 - at)) >> 31));
       }
     }
   }
@@ -139,9 +153,8 @@ __global__ __launch_bounds__(256, OCC) void k_mx_grad(const GradArgs g) {
       store_rows<false, T::PB>(t.acc, buf, part, g.nf, row0, g.ns, c0, g.nf, false, StoreAsIs());
     } else {
       constexpr int V = YBF16 ? 8 : 4;
-      constexpr int PB = MASK != 0 && !YBF16 ? 1 : T::PB;  // fewer rows at a time where each brings a mask's registers too
-      StoreMasked<MASK, V, 16 * PB / V> done = {g, {}, {}};
-      store_rows<YBF16, PB>(t.acc, buf, g.Y, g.ld, row0, g.ns, c0, g.nf, g.accumulate, done);
+      StoreMasked<MASK, V, 16 * T::PB / V, MB / T::PB * NB> done = {g, {}, {}, {}};
+      store_rows<YBF16, T::PB>(t.acc, buf, g.Y, g.ld, row0, g.ns, c0, g.nf, g.accumulate, done);
     }
     if (!T::STAYS) return;
     t.clear();
@@ -162,12 +175,10 @@ __global__ __launch_bounds__(256) void k_mx_grad_join(const GradArgs g, const fl
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         if (c + q < g.nf) v[q] += part[s * stride + row * g.nf + c + q];
-    StoreMasked<MASK, 4, 1> done = {g, {}, {}};
-    done.row(0, 0, row, c);
-    done.finish(0, 0, v);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       if (c + q >= g.nf) continue;
+      v[q] = masked<MASK>(g, row, c + q, v[q]);
       if (YBF16) {
         static_cast<uint16_t*>(g.Y)[row * g.ld + c + q] = (uint16_t)bf16_bits(v[q]);
       } else {
@@ -259,8 +270,9 @@ GradPlan grad_plan(int64_t ns, int64_t nf, int64_t nk) {
   GradPlan p = {0, 1, std::max<int64_t>(64, (int64_t)align_up(nk, 64))};
   auto tiles = [&](int64_t w) { return ceil_div(ns, w) * ceil_div(nf, w); };
   // us with tiles of 64 / 128 / 256 (dX): 512 x 4096 x 4096 48 / 54 / 96, 1024 x 4096 x 4096 66 / 58 / 100,
-  // 2048 x 4096 x 4096 109 / 75 / 91, 4096 x 4096 x 4096 200 / 131 / 114, 1500 x 2000 x 3000 (192 tiles of 128) 42 / 50 / -
-  p.tile = tiles(256) >= 192 ? 2 : tiles(128) >= 224 ? 1 : 0;
+  // 2048 x 4096 x 4096 109 / 75 / 91, 4096 x 4096 x 4096 200 / 131 / 114, 1500 x 2000 x 3000 (192 tiles of 128) 42 / 50 / -,
+  // 8000 x 8000 x 256 87 / 61 / 68, 8000 x 8000 x 1024 224 / 144 / 134
+  p.tile = tiles(256) >= 192 && nk >= 512 ? 2 : tiles(128) >= 224 ? 1 : 0;
   // Slices of k, joined by another launch, where the tiles leave places of the chip empty (three 64 x 64 tiles fit a CU)
   // and each slice has a long sum: 200 x 4096 x 4096 takes 37 us with 4 and 47 with one, dW 4096 x 1024 x 1024 36 and 44,
   // but 512 x 1024 x 1024 15.5 with two and 14.0 with one.

@@ -435,10 +435,10 @@ static inline unsigned tile_grid(int64_t tiles, int places) {
 //
 // The code of this part counts: it runs once a tile, and comes from memory if it is long (with the edges' cases expanded
 // for each block it grew to 90 KB, and the 4-bit product at 16384 x 4096 x 11008 took 446 us instead of 390). Blocks
-// inside Y take 16-byte stores, a lane completing V consecutive columns of IT rows: done.columns(c) is called for each
-// new c, done.row(set, it, row, c) for each row of the next block, done.settle(set) before a block's first store and
-// done.finish(set, it, v) to complete its results. Blocks at an edge go one column a lane
-// by done.one(row, c, v).
+// inside Y take 16-byte stores, a lane completing V consecutive columns of IT rows: done.row(set, it, row, c) fetches what
+// a row needs and done.keep(set, b) what remains of it for block b, before the first store; done.columns(c) is called for
+// each new c and done.finish(b, it, v) completes the results. Blocks at an edge go one column a lane by
+// done.one(row, c, v).
 template <bool YBF16, int PB, int MB, int NB, typename D>
 __device__ __forceinline__ void store_rows(const f32x16 (&acc)[MB][NB], uint8_t* lds, void* __restrict__ Y, int64_t ld,
                                            int64_t row0, int64_t rows, int c0, int cols, bool add, D&& done) {
@@ -449,13 +449,22 @@ __device__ __forceinline__ void store_rows(const f32x16 (&acc)[MB][NB], uint8_t*
   const bool inside = row0 + 32 * NB <= rows && c0 + 32 * MB <= cols;
   // the 16-byte chunks of row r are permuted by XOR with r, so that neither side's rows meet on the same banks
   auto chunk = [](int row, int q) { return row * C + ((q ^ (row & (C / 4 - 1))) << 2); };
-  auto fetch = [&](int b) {  // what block b's rows need, into set b % 2
-    const int64_t first = row0 + b % NB * 32 + lane / PER_ROW;
-    const int c = c0 + 32 * PB * (b / NB) + (lane % PER_ROW) * V;
+  // What the rows need is all fetched before the first store: loads and stores end in their order, so a load behind a store
+  // would wait for it.
+  if (inside) {
+    constexpr int BLOCKS = MB / PB * NB, BATCH = BLOCKS < 4 ? BLOCKS : 4;
 #pragma unroll
-    for (int it = 0; it < IT; ++it) done.row(b % 2, it, first + it * STEP, c);
-  };
-  if (inside) fetch(0);
+    for (int b0 = 0; b0 < BLOCKS; b0 += BATCH) {
+#pragma unroll
+      for (int b = b0; b < b0 + BATCH; ++b)
+#pragma unroll
+        for (int it = 0; it < IT; ++it)
+          done.row(b % BATCH, it, row0 + b % NB * 32 + lane / PER_ROW + it * STEP,
+                   c0 + 32 * PB * (b / NB) + (lane % PER_ROW) * V);
+#pragma unroll
+      for (int b = b0; b < b0 + BATCH; ++b) done.keep(b % BATCH, b);
+    }
+  }
 #pragma unroll
   for (int m0 = 0; m0 < MB; m0 += PB) {
     const int c = c0 + 32 * m0 + (lane % PER_ROW) * V;
@@ -464,7 +473,6 @@ __device__ __forceinline__ void store_rows(const f32x16 (&acc)[MB][NB], uint8_t*
     for (int nb = 0; nb < NB; ++nb) {
       const int b = m0 / PB * NB + nb;
       const int64_t first = row0 + nb * 32 + lane / PER_ROW;
-      if (inside && b + 1 < MB / PB * NB) fetch(b + 1);
 #pragma unroll
       for (int mb = 0; mb < PB; ++mb)
 #pragma unroll
@@ -473,7 +481,6 @@ __device__ __forceinline__ void store_rows(const f32x16 (&acc)[MB][NB], uint8_t*
               make_float4(acc[m0 + mb][nb][4 * g], acc[m0 + mb][nb][4 * g + 1], acc[m0 + mb][nb][4 * g + 2],
                           acc[m0 + mb][nb][4 * g + 3]);
       __builtin_amdgcn_wave_barrier();
-      done.settle(b % 2);
       if (inside) {
 #pragma unroll
         for (int it = 0; it < IT; ++it) {
@@ -484,7 +491,7 @@ __device__ __forceinline__ void store_rows(const f32x16 (&acc)[MB][NB], uint8_t*
                 buf + chunk(lane / PER_ROW + it * STEP, (lane % PER_ROW) * (V / 4) + q));
             v[4 * q] = x.x, v[4 * q + 1] = x.y, v[4 * q + 2] = x.z, v[4 * q + 3] = x.w;
           }
-          done.finish(b % 2, it, v);
+          done.finish(b, it, v);
           const int64_t at = (first + it * STEP) * ld + c;
           if (YBF16) {
             *reinterpret_cast<i32x4_any*>(static_cast<uint16_t*>(Y) + at) =
@@ -523,7 +530,7 @@ __device__ __forceinline__ void store_rows(const f32x16 (&acc)[MB][NB], uint8_t*
 struct StoreAsIs {
   __device__ __forceinline__ void columns(int) {}
   __device__ __forceinline__ void row(int, int, int64_t, int) {}
-  __device__ __forceinline__ void settle(int) {}
+  __device__ __forceinline__ void keep(int, int) {}
   __device__ __forceinline__ float one(int64_t, int, float v) { return v; }
   template <int V>
   __device__ __forceinline__ void finish(int, int, float (&)[V]) {}
