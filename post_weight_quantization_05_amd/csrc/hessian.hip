@@ -408,9 +408,12 @@ struct DmaCtx {
 // buffer_load_dwordx4 ... lds: 64 lanes x 16 B to LDS[m0 + lane * 16]. Written as inline asm so that the
 // compiler does not add its own (conservative, vmcnt(0)) waits before every LDS read that follows; the
 // stage pipeline orders the DMA with explicit vmcnt waits and barriers, and the main loop issues no other
-// vector-memory instruction.
+// vector-memory instruction. Nor does it look into the asm for the waits that the hardware leaves to software:
+// one state from the write of M0 to the load (the s_nop; without it a load may take the M0 of the one before),
+// and five from a vector instruction that wrote a scalar register of the load, of which none comes that close in
+// what is built (tests/test_isa_host.py checks both).
 __device__ __forceinline__ void dma16(const i32x4& rsrc, uint32_t lds_addr, uint32_t voff) {
-  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                :
                : "s"(lds_addr), "v"(voff), "s"(rsrc)
                : "memory", "m0");

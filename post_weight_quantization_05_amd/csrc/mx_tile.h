@@ -39,18 +39,22 @@ __device__ __forceinline__ void static_for(F&& f) {
 
 // buffer_load_dwordx4 ... lds: 64 lanes x 16 B to LDS[addr + lane * 16]; out-of-range reads arrive as zeros. Inline asm,
 // so that the compiler adds no waits of its own; no register is written, and the ring orders the transfers with
-// explicit vmcnt waits and barriers.
+// explicit vmcnt waits and barriers. The compiler does not look into the asm for the waits that the hardware leaves to
+// software. A load to LDS needs one state after the write of M0: the s_nop (without it a load may take the M0 of the
+// transfer before, and its kilobyte lands there). It also needs five after a vector instruction that wrote one of its
+// scalar registers, as a spilled one's return does: none comes that close in what is built, which
+// tests/test_isa_host.py checks (s_nop 4 would cover it here, but costs dX 8192 x 11008 x 4096 638 us instead of 619).
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"  // m0 is a reserved register; it is named as clobbered all the same
 __device__ __forceinline__ void dma16(const i32x4& rsrc, uint32_t lds_addr, uint32_t voff) {
-  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                :
                : "s"(lds_addr), "v"(voff), "s"(rsrc)
                : "memory", "m0");
 }
 // the same where `skip` is 0; a branch of the compiler's would let it move products across the ring's barriers
 __device__ __forceinline__ void dma16_unless(int skip, const i32x4& rsrc, uint32_t lds_addr, uint32_t voff) {
-  asm volatile("s_cmp_lg_u32 %3, 0\n\ts_cbranch_scc1 .Lno_transfer%=\n\ts_mov_b32 m0, %0\n\t"
+  asm volatile("s_cmp_lg_u32 %3, 0\n\ts_cbranch_scc1 .Lno_transfer%=\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\t"
                "buffer_load_dwordx4 %1, %2, 0 offen lds\n.Lno_transfer%=:"
                :
                : "s"(lds_addr), "v"(voff), "s"(rsrc), "s"(skip)
