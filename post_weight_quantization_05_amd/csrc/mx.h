@@ -74,9 +74,11 @@ __device__ __forceinline__ uint32_t bf16_bits(float v) {
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) { return bf16_bits(lo) | (bf16_bits(hi) << 16); }
 
 // Parts of an E4M3 fragment whose exponents differ by at most 7: codes with the top exponent bit set, and the rest.
-// The matrix core aligns the products of one instruction to their largest and drops what lies more than about 13
-// bits below; with half of the exponents to each part nothing is dropped against E2M1 weights, so the sum is exact
-// up to fp32 rounding.
+// The matrix core aligns the products of a block to the largest of them and drops what lies more than about 13 bits below
+// (256 x 6 - 256 x 6 + 1/8 x 1/2 comes out as 0); with half of the exponents to each part nothing is dropped against E2M1
+// weights (which span 7 bits against each other), so the sum is exact up to fp32 rounding. Blocks are added in fp32, however
+// far their scales lie apart. Two instructions a product cost twice the matrix cores' time: 2048 x 4096 x 11008 takes 158 us,
+// and 88 with one, whose results lie 2.6e-4 off.
 __device__ __forceinline__ void split_e4m3(const i32x8& a, i32x8& hi, i32x8& lo) {
 #pragma unroll
   for (int q = 0; q < 8; ++q) {

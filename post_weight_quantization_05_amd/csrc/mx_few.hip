@@ -116,7 +116,7 @@ __device__ __forceinline__ void few_load(FewPart<SRC>& p, const FewSource<FMT, S
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int j) { return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w; }
 
 // the J-th 128 columns of the part
-template <int FMT, int SRC, bool SPLIT, int J>
+template <int FMT, int SRC, int J>
 __device__ __forceinline__ void few_multiply(const FewPart<SRC>& p, int g, f32x4& acc) {
   i32x8 x = {0, 0, 0, 0, 0, 0, 0, 0};
   uint32_t byte;  // in the low 8 bits; 255 makes its products NaN whatever the codes
@@ -156,7 +156,7 @@ __device__ __forceinline__ void few_multiply(const FewPart<SRC>& p, int g, f32x4
   const i32x8 w = {(int)p.w[J].x, (int)p.w[J].y, (int)p.w[J].z, (int)p.w[J].w, 0, 0, 0, 0};
   const int ws = (int)(word_of(p.s, J) >> (8 * g));
   constexpr int FB = FMT == GPTQ_MX_E2M1 ? 4 : 0;
-  if constexpr (SPLIT) {
+  if constexpr (FMT == GPTQ_MX_E4M3) {
     i32x8 hi, lo;
     split_e4m3(x, hi, lo);
     acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, lo, acc, 4, FB, 0, ws, 0, (int)byte);
@@ -168,7 +168,6 @@ __device__ __forceinline__ void few_multiply(const FewPart<SRC>& p, int g, f32x4
 
 template <int FMT, int SRC, bool VEC, bool YBF16>
 __global__ __launch_bounds__(64 * FEW_WAVES) void k_mx_few(const FewArgs a) {
-  constexpr bool SPLIT = FMT == GPTQ_MX_E4M3 && !YBF16;
   __shared__ float red[FEW_WAVES][16][20];
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -182,10 +181,10 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void k_mx_few(const FewArgs a) {
   for (int u = wave; u < units; u += FEW_WAVES) {
     few_load<FMT, SRC, VEC>(part, src, a, u, chunks, r);
     __builtin_amdgcn_sched_barrier(0);  // all loads first
-    few_multiply<FMT, SRC, SPLIT, 0>(part, g, acc);
-    if (4 * u + 1 < chunks) few_multiply<FMT, SRC, SPLIT, 1>(part, g, acc);
-    if (4 * u + 2 < chunks) few_multiply<FMT, SRC, SPLIT, 2>(part, g, acc);
-    if (4 * u + 3 < chunks) few_multiply<FMT, SRC, SPLIT, 3>(part, g, acc);
+    few_multiply<FMT, SRC, 0>(part, g, acc);
+    if (4 * u + 1 < chunks) few_multiply<FMT, SRC, 1>(part, g, acc);
+    if (4 * u + 2 < chunks) few_multiply<FMT, SRC, 2>(part, g, acc);
+    if (4 * u + 3 < chunks) few_multiply<FMT, SRC, 3>(part, g, acc);
   }
   // register i of lane 16 g + r: W's row 4 g + i, token r
   *reinterpret_cast<float4*>(&red[wave][r][4 * g]) = make_float4(acc[0], acc[1], acc[2], acc[3]);

@@ -48,9 +48,9 @@ struct StoreLinear {
   __device__ __forceinline__ float one(int64_t, int c, float v) { return relu(bias ? v + bias[c] : v); }
 };
 
-template <int FMT, bool SPLIT, bool YBF16, int WA, int WB, int MB, int NB, int OCC>
+template <int FMT, bool YBF16, int WA, int WB, int MB, int NB, int OCC>
 __global__ __launch_bounds__(256, OCC) void k_mx_matmul(const MatmulArgs g) {
-  using T = TileProduct<K_E2M1, FMT == GPTQ_MX_E2M1 ? K_E2M1 : K_E4M3, WA, WB, MB, NB, SPLIT>;
+  using T = TileProduct<K_E2M1, FMT == GPTQ_MX_E2M1 ? K_E2M1 : K_E4M3, WA, WB, MB, NB>;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS];
   TileOrder order;
   order.init(blockIdx.x, gridDim.x, g.ta, g.tb);
@@ -129,7 +129,8 @@ MatmulPlan matmul_plan(int64_t n, int64_t in, int64_t out, int fmt) {
   auto tiles = [&](int64_t a, int64_t b) { return ceil_div(out, a) * ceil_div(n, b); };
   // The largest tile that gives (nearly) every CU one. us with tiles of 64 / 128 / 256 (E2M1): 512 x 4096 x 4096 13.1 /
   // 13.8 / 26, 1024 x 4096 x 4096 21.3 / 16.9 / 32, 2048 x 4096 x 4096 37 / 26 / 35, 4096 x 4096 x 4096 67 / 47 / 42; with a
-  // short k the results' way out counts more than the products: 8000 x 1024 x 8000 92 / 64 / 74 (E4M3 118 / 100 / 83).
+  // short k the results' way out counts more than the products: 8000 x 1024 x 8000 92 / 64 / 74. E4M3: 512 x 4096 x 4096
+  // 23 / 19 / 48, 1024 x 4096 x 4096 40 / 31 / 51, 4096 x 4096 x 4096 143 / 115 / 113, 8000 x 1024 x 8000 169 / 138 / 138.
   MatmulPlan p = {64, 64, 1};
   if (fmt == GPTQ_MX_E2M1) {
     if (tiles(256, 256) >= 256 && nk >= 16) p = {256, 256, 1};
@@ -145,10 +146,10 @@ MatmulPlan matmul_plan(int64_t n, int64_t in, int64_t out, int fmt) {
   return p;
 }
 
-template <int FMT, bool SPLIT, bool YBF16>
+template <int FMT, bool YBF16>
 void matmul_go(const MatmulPlan& p, dim3 grid, hipStream_t stream, const MatmulArgs& g) {
 #define GPTQ_GO(WA, WB, MB, NB, OCC) \
-  hipLaunchKernelGGL((k_mx_matmul<FMT, SPLIT, YBF16, WA, WB, MB, NB, OCC>), grid, dim3(256), 0, stream, g)
+  hipLaunchKernelGGL((k_mx_matmul<FMT, YBF16, WA, WB, MB, NB, OCC>), grid, dim3(256), 0, stream, g)
   if (p.wa == 64) {
     GPTQ_GO(64, 64, 1, 1, 2);
   } else if constexpr (FMT == GPTQ_MX_E2M1) {
@@ -191,11 +192,9 @@ hipError_t mx_matmul_launch(const MxMatrix& a, const MxMatrix& w, const float* b
     if (slices > 1) g.Y = ws, g.ld = w.rows;
     const dim3 grid(tile_grid((int64_t)g.ta * g.tb, p.wa == 256 ? 256 : 1 << 30), (unsigned)slices);
     if (a.fmt == GPTQ_MX_E2M1) {
-      bf16 ? matmul_go<GPTQ_MX_E2M1, false, true>(p, grid, stream, g)
-           : matmul_go<GPTQ_MX_E2M1, false, false>(p, grid, stream, g);
+      bf16 ? matmul_go<GPTQ_MX_E2M1, true>(p, grid, stream, g) : matmul_go<GPTQ_MX_E2M1, false>(p, grid, stream, g);
     } else {
-      bf16 ? matmul_go<GPTQ_MX_E4M3, false, true>(p, grid, stream, g)
-           : matmul_go<GPTQ_MX_E4M3, true, false>(p, grid, stream, g);
+      bf16 ? matmul_go<GPTQ_MX_E4M3, true>(p, grid, stream, g) : matmul_go<GPTQ_MX_E4M3, false>(p, grid, stream, g);
     }
   }
   if (slices > 1) {

@@ -104,7 +104,7 @@ struct StoreMasked {
 
 template <bool GRAD_INPUT, bool YBF16, int MASK, int WA, int WB, int MB, int NB, int OCC>
 __global__ __launch_bounds__(256, OCC) void k_mx_grad(const GradArgs g) {
-  using T = TileProduct<K_BF16T, GRAD_INPUT ? K_BF16 : K_BF16T, WA, WB, MB, NB, false>;
+  using T = TileProduct<K_BF16T, GRAD_INPUT ? K_BF16 : K_BF16T, WA, WB, MB, NB>;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS];
   if (!GRAD_INPUT && g.db && blockIdx.y == 0) {
     for (int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x; c < g.ns; c += (int64_t)gridDim.x * 256) {

@@ -197,8 +197,8 @@ __device__ __forceinline__ i32x8 as_operand(const int (&f)[N]) {
 }
 
 // A (first operand) x B (second): KA is K_E2M1 with KB K_E2M1 or K_E4M3, or both are bf16 kinds.
-// SPLIT: E4M3 fragments in two parts (see split_e4m3).
-template <int KA, int KB, int WA, int WB, int MB, int NB, bool SPLIT>
+// E4M3 fragments are multiplied in two parts (see split_e4m3).
+template <int KA, int KB, int WA, int WB, int MB, int NB>
 struct TileProduct {
   static constexpr int NW = 4;
   static constexpr bool MX = KA == K_E2M1;
@@ -325,7 +325,7 @@ struct TileProduct {
     } else {
       constexpr int FB = KB == K_E2M1 ? 4 : 0, Q = J >> 1, OS = 2 * (J & 1);
       const i32x8 x = as_operand<KA>(fa[SET][M]), y = as_operand<KB>(fb[SET][N]);
-      if constexpr (SPLIT) {
+      if constexpr (KB == K_E4M3) {
         i32x8 hi, lo;
         split_e4m3(y, hi, lo);
         acc[M][N] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, lo, acc[M][N], 4, FB, OS, sca[M][Q], OS, scb[N][Q]);
