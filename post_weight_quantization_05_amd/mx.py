@@ -187,7 +187,8 @@ def mx_quantize(X: torch.Tensor, fmt: str = "e2m1", stream=None) -> MXTensor:
     code = _fmt_code(fmt)
     _req_cuda(X, "X")
     if X.dim() == 3:
-        X = X.reshape(-1, X.shape[-1])
+        with _on(stream):  # tokens that no view flattens are copied there, and the copy belongs to it
+            X = X.reshape(-1, X.shape[-1])
     ld = _matrix(X, "X")
     n, d = X.shape
     xt = _dtype_code(X)
