@@ -91,7 +91,8 @@ def hessian_accumulate(X: torch.Tensor, state: HessianState, stream=None) -> Hes
     to tokens as the handbook's compute_hessian does)."""
     _req_cuda(X, "X")
     if X.dim() == 3:
-        X = X.reshape(-1, X.shape[-1])
+        with _on(stream):  # tokens that no view flattens are copied there, and the copy belongs to it
+            X = X.reshape(-1, X.shape[-1])
     ld = _ld(X, "X")
     code = _dtype_code(X)
     n_rows, d_in = X.shape

@@ -1,4 +1,4 @@
-"""MX operators on tensors and streams of other kinds than the current one's."""
+"""Calls on another stream than the current one, with tokens that have to be copied to be flattened."""
 import pytest
 import torch
 
@@ -28,3 +28,21 @@ def test_quantize_of_transposed_tokens_on_a_side_stream(fmt):
         for q in got:
             assert torch.equal(q.codes, want.codes) and torch.equal(q.scales, want.scales)
         del junk
+
+
+def test_hessian_of_transposed_tokens_on_a_side_stream():
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn((64, 40, 256), generator=g, device="cuda").bfloat16()
+    want = G.hessian_accumulate(x.transpose(0, 1).contiguous(), G.HessianState(256))
+    busy = torch.randn((4096, 4096), generator=g, device="cuda")
+    side = torch.cuda.Stream()
+    state = G.HessianState(256, stream=side)
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(4):
+        busy = busy @ busy * 1e-2
+    G.hessian_accumulate(x.transpose(0, 1), state, stream=side)
+    junk = [torch.full((64 * 40, 256), 9.0, dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+    torch.cuda.synchronize()
+    assert torch.equal(state.S.tril(), want.S.tril()) and torch.equal(state.colsq, want.colsq)
+    assert state.n_total == want.n_total == 64 * 40
+    del junk

@@ -61,3 +61,11 @@ def test_mx_quantize_flattens_tokens_on_its_stream(recorder, fmt):
         q = mx.mx_quantize(x, fmt, stream=types.SimpleNamespace(cuda_stream=1))
     assert q.shape == (12, 64)
     assert not recorder.outside(COPIES | ALLOCATIONS) and recorder.inside(COPIES), recorder.calls
+
+
+def test_hessian_accumulate_flattens_tokens_on_its_stream(recorder):
+    x = torch.zeros(4, 3, 64).transpose(0, 1)
+    state = gptq.HessianState(64, device="cpu")
+    with recorder:
+        gptq.hessian_accumulate(x, state, stream=types.SimpleNamespace(cuda_stream=1))
+    assert not recorder.outside(COPIES | ALLOCATIONS) and recorder.inside(COPIES), recorder.calls
