@@ -10,8 +10,8 @@ A training step through one layer, with only the 8-bit checkpoint kept between i
     dx = mx_grad_input(dy, w, mask=a)              # mask: x came out of a ReLU
     dw, db = mx_grad_weight(dy, a, bias_grad=True)
 
-Every call is asynchronous on `stream` (None = the current stream), allocates its results and workspace there, and
-can be captured into a graph.
+Every call is asynchronous on `stream` (None = the current stream of the tensors' device), allocates its results and
+workspace there, and can be captured into a graph.
 """
 from __future__ import annotations
 
@@ -90,6 +90,19 @@ def _stream(stream, device_index: int) -> int:
     if stream is None and _raw_stream is not None:
         return _raw_stream(device_index)
     return _stream_handle(stream)
+
+
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _call(name: str, device: int, *args) -> None:
+    """The library's function with that device as the current one, on which its kernels are launched."""
+    f = getattr(_lib.load(), name)
+    if _current_device() == device:
+        check(f(*args), name)
+    else:
+        with torch.cuda.device(device):
+            check(f(*args), name)
 
 
 def _empty(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
@@ -194,8 +207,9 @@ def mx_quantize(X: torch.Tensor, fmt: str = "e2m1", stream=None) -> MXTensor:
     xt = _dtype_code(X)
     codes = _empty((n, _code_row(d, fmt)), torch.uint8, X, stream)
     scales = _empty((n, _scale_row(d)), torch.uint8, X, stream)
-    check(_lib.load().gptq_mx_quantize(X.data_ptr(), xt, n, d, ld, code, codes.data_ptr(), scales.data_ptr(),
-                                       _stream(stream, X.get_device())), "gptq_mx_quantize")
+    dev = X.get_device()
+    _call("gptq_mx_quantize", dev, X.data_ptr(), xt, n, d, ld, code, codes.data_ptr(), scales.data_ptr(),
+          _stream(stream, dev))
     return MXTensor(codes, scales, d, fmt)
 
 
@@ -204,8 +218,9 @@ def mx_dequantize(Q: MXTensor, dtype=torch.bfloat16, out: torch.Tensor | None = 
     code, yt = _mx(Q, "Q"), _out_code(dtype)
     c, n, d = Q.codes, Q.codes.shape[0], Q.cols
     Y, ld = _result(out, "out", (n, d), dtype, c, stream)
-    check(_lib.load().gptq_mx_dequantize(c.data_ptr(), Q.scales.data_ptr(), code, n, d, Y.data_ptr(), yt, ld,
-                                         _stream(stream, c.get_device())), "gptq_mx_dequantize")
+    dev = c.get_device()
+    _call("gptq_mx_dequantize", dev, c.data_ptr(), Q.scales.data_ptr(), code, n, d, Y.data_ptr(), yt, ld,
+          _stream(stream, dev))
     return Y
 
 
@@ -222,9 +237,8 @@ def mx_matmul(A: MXTensor, W: MXTensor, bias: torch.Tensor | None = None, relu: 
     Y, ld = _result(out, "out", (n, no), dtype, c, stream)
     need = _need("gptq_mx_matmul_workspace_bytes", n, d, no, code)
     ws, wp = _workspace(need, c, stream)
-    check(_lib.load().gptq_mx_matmul(c.data_ptr(), A.scales.data_ptr(), code, n, d, W.codes.data_ptr(),
-                                     W.scales.data_ptr(), no, b, 1 if relu else 0, Y.data_ptr(), yt, ld, wp, need,
-                                     _stream(stream, dev)), "gptq_mx_matmul")
+    _call("gptq_mx_matmul", dev, c.data_ptr(), A.scales.data_ptr(), code, n, d, W.codes.data_ptr(), W.scales.data_ptr(),
+          no, b, 1 if relu else 0, Y.data_ptr(), yt, ld, wp, need, _stream(stream, dev))
     return Y
 
 
@@ -244,9 +258,8 @@ def mx_linear(X: torch.Tensor, W: MXTensor, act: str = "e4m3", bias: torch.Tenso
     Y, ld = _result(out, "out", (n, no), dtype, X, stream)
     need = _need("gptq_mx_linear_workspace_bytes", n, d, no, code)
     ws, wp = _workspace(need, X, stream)
-    check(_lib.load().gptq_mx_linear(X.data_ptr(), xt, n, d, ldx, code, W.codes.data_ptr(), W.scales.data_ptr(), no, b,
-                                     1 if relu else 0, Y.data_ptr(), yt, ld, wp, need, _stream(stream, dev)),
-          "gptq_mx_linear")
+    _call("gptq_mx_linear", dev, X.data_ptr(), xt, n, d, ldx, code, W.codes.data_ptr(), W.scales.data_ptr(), no, b,
+          1 if relu else 0, Y.data_ptr(), yt, ld, wp, need, _stream(stream, dev))
     return Y
 
 
@@ -274,9 +287,8 @@ def mx_grad_input(dY: torch.Tensor, W: MXTensor, mask: MXTensor | None = None, d
     dX, ld = _result(out, "out", (n, d), dtype, dY, stream)
     need = _need("gptq_mx_grad_input_workspace_bytes", n, d, no)
     ws, wp = _workspace(need, dY, stream)
-    check(_lib.load().gptq_mx_grad_input(dY.data_ptr(), ldy, n, no, W.codes.data_ptr(), W.scales.data_ptr(), d, mc, ms,
-                                         mt, dX.data_ptr(), yt, ld, wp, need, _stream(stream, dev)),
-          "gptq_mx_grad_input")
+    _call("gptq_mx_grad_input", dev, dY.data_ptr(), ldy, n, no, W.codes.data_ptr(), W.scales.data_ptr(), d, mc, ms, mt,
+          dX.data_ptr(), yt, ld, wp, need, _stream(stream, dev))
     return dX
 
 
@@ -302,7 +314,6 @@ def mx_grad_weight(dY: torch.Tensor, A: MXTensor, bias_grad: bool = False, dtype
         dbp = db.data_ptr() if bias_out is None else _bias_ptr(db, no, dY)
     need = _need("gptq_mx_grad_weight_workspace_bytes", n, d, no)
     ws, wp = _workspace(need, dY, stream)
-    check(_lib.load().gptq_mx_grad_weight(dY.data_ptr(), ldy, n, no, A.codes.data_ptr(), A.scales.data_ptr(), code, d,
-                                          1 if accumulate else 0, dW.data_ptr(), wt, ld, dbp, wp, need,
-                                          _stream(stream, dev)), "gptq_mx_grad_weight")
+    _call("gptq_mx_grad_weight", dev, dY.data_ptr(), ldy, n, no, A.codes.data_ptr(), A.scales.data_ptr(), code, d,
+          1 if accumulate else 0, dW.data_ptr(), wt, ld, dbp, wp, need, _stream(stream, dev))
     return dW, db

@@ -50,6 +50,7 @@ def recorder(monkeypatch):
     for m in (gptq, mx):
         monkeypatch.setattr(m, "_on", r.on)
         monkeypatch.setattr(m, "_req_cuda", lambda t, name: None)
+    monkeypatch.setattr(mx, "_current_device", lambda: -1, raising=False)  # get_device() of a host tensor
     monkeypatch.setattr(_lib, "load", lambda path=None: _Library())
     return r
 
@@ -69,3 +70,56 @@ def test_hessian_accumulate_flattens_tokens_on_its_stream(recorder):
     with recorder:
         gptq.hessian_accumulate(x, state, stream=types.SimpleNamespace(cuda_stream=1))
     assert not recorder.outside(COPIES | ALLOCATIONS) and recorder.inside(COPIES), recorder.calls
+
+
+class _OnDevice1(torch.Tensor):
+    """A host tensor that says it lies on device 1."""
+    is_cuda = property(lambda self: True)
+
+    def get_device(self):
+        return 1
+
+
+def _calls():
+    def t(shape, dtype=torch.uint8):
+        return torch.zeros(shape, dtype=dtype).as_subclass(_OnDevice1)
+
+    a = mx.MXTensor(t((40, 128)), t((40, 16)), 64, "e4m3")
+    w = mx.MXTensor(t((8, 64)), t((8, 16)), 64, "e2m1")
+    x, dy = t((40, 64), torch.bfloat16), t((40, 8), torch.bfloat16)
+    s = types.SimpleNamespace(cuda_stream=1)
+    return {
+        "gptq_mx_quantize": lambda: mx.mx_quantize(x, stream=s),
+        "gptq_mx_dequantize": lambda: mx.mx_dequantize(a, stream=s),
+        "gptq_mx_matmul": lambda: mx.mx_matmul(a, w, stream=s),
+        "gptq_mx_linear": lambda: mx.mx_linear(x, w, stream=s),
+        "gptq_mx_grad_input": lambda: mx.mx_grad_input(dy, w, mask=a, stream=s),
+        "gptq_mx_grad_weight": lambda: mx.mx_grad_weight(dy, a, bias_grad=True, stream=s),
+    }
+
+
+@pytest.mark.parametrize("current", [0, 1])
+@pytest.mark.parametrize("name", list(_calls()))
+def test_mx_calls_run_on_their_tensors_device(monkeypatch, recorder, name, current):
+    """The library launches on the current device: a call on another device's tensors makes that one current."""
+    device, seen = [current], []
+
+    @contextlib.contextmanager
+    def use(d):
+        device.append(d)
+        yield
+        device.pop()
+
+    class Library(_Library):
+        def __getattr__(self, f):
+            if f.endswith("_bytes"):
+                return lambda *a: 256
+            return lambda *a: seen.append((f, device[-1])) or 0
+
+    monkeypatch.setattr(_lib, "load", lambda path=None: Library())
+    monkeypatch.setattr(mx, "_current_device", lambda: device[-1], raising=False)
+    monkeypatch.setattr(torch.cuda, "device", use)
+    mx._need.cache_clear()
+    _calls()[name]()
+    mx._need.cache_clear()
+    assert seen == [(name, 1)] and device == [current]
