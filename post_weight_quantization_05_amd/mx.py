@@ -11,7 +11,8 @@ A training step through one layer, with only the 8-bit checkpoint kept between i
     dw, db = mx_grad_weight(dy, a, bias_grad=True)
 
 Every call is asynchronous on `stream` (None = the current stream of the tensors' device), allocates its results and
-workspace there, and can be captured into a graph.
+workspace there, and can be captured into a graph. No call records an autograd graph, whatever its inputs require: the
+gradients are calls of their own.
 """
 from __future__ import annotations
 
@@ -272,7 +273,8 @@ def _grad(dY: torch.Tensor) -> int:
 def mx_grad_input(dY: torch.Tensor, W: MXTensor, mask: MXTensor | None = None, dtype=torch.bfloat16,
                   out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """dX = dY W (dY n x out bf16, W out x in e2m1), zero wherever `mask` (n x in, the checkpoint of a ReLU's
-    outputs) is not positive."""
+    outputs) is not positive. An activation that the checkpoint rounded to 0 counts as 0: in e4m3 at least 2.2e5 times
+    below its block's largest, in e2m1 up to 1/16 of it."""
     ldy = _grad(dY)
     n, no = dY.shape
     dev = dY.get_device()
