@@ -147,11 +147,13 @@ def _w4(t: MXTensor, name: str, device: int | None = None, cols: int | None = No
 
 
 def _result(out, name: str, shape, dtype, like: torch.Tensor, stream):
-    """The result's tensor and its leading dimension."""
+    """The result's tensor and its leading dimension. like: the first operand."""
     if out is None:
         return _empty(shape, dtype, like, stream), shape[1]
     if not out.is_cuda or out.device != like.device or out.dtype != dtype or tuple(out.shape) != tuple(shape):
         raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {like.device}")
+    if out.numel() and out.data_ptr() == like.data_ptr():
+        raise ValueError(f"{name} is an operand: results lie apart from what other workgroups still read")
     return out, _row_stride(out, name)
 
 

@@ -123,3 +123,19 @@ def test_mx_calls_run_on_their_tensors_device(monkeypatch, recorder, name, curre
     _calls()[name]()
     mx._need.cache_clear()
     assert seen == [(name, 1)] and device == [current]
+
+
+def test_mx_results_are_no_operands(monkeypatch, recorder):
+    """A result written over an operand would race with the workgroups that still read it."""
+    monkeypatch.setattr(mx, "_current_device", lambda: 1)
+
+    def t(shape, dtype=torch.uint8):
+        return torch.zeros(shape, dtype=dtype).as_subclass(_OnDevice1)
+
+    w = mx.MXTensor(t((64, 64)), t((64, 16)), 64, "e2m1")
+    x = t((40, 64), torch.bfloat16)
+    s = types.SimpleNamespace(cuda_stream=1)
+    for call in (lambda out: mx.mx_linear(x, w, out=out, stream=s), lambda out: mx.mx_grad_input(x, w, out=out, stream=s)):
+        with pytest.raises(ValueError, match="operand"):
+            call(x)
+        assert call(torch.zeros_like(x)).shape == x.shape
