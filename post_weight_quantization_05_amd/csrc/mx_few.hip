@@ -10,7 +10,7 @@
 //
 // Few tokens are quantized by every workgroup in registers, in that layout (a lane loads just the columns whose codes it
 // holds), which saves a launch; more of them (mx_few_fused) in a launch of their own, since every workgroup would load and
-// convert them all. 1 x 4096 x 4096 takes 5.0 us of which an empty kernel takes 2.7, 12 x 11008 x 4096 12.9 us.
+// convert them all. 1 x 4096 x 4096 takes 4.8 us of which an empty kernel takes 2.7, 12 x 11008 x 4096 12.7 us with that.
 #include <algorithm>
 
 #include "mx_codec.h"
