@@ -101,7 +101,9 @@ def check_scalars(lines):
         if re.match(r"buffer_(load|store|atomic)", ins):
             reads = set().union(*(_scalars(o.split()[0]) for o in _operands(ins) if o))
             for w in _before(lines, i, 5):
-                if w.startswith("v_") and _operands(w) and _scalars(_operands(w)[0]) & reads:
+                # carries and the like go to a second result
+                results = _operands(w)[:2 if re.match(r"v_\w*(_co_|div_scale|_mad_[iu]64)", w) else 1]
+                if w.startswith("v_") and any(_scalars(r) & reads for r in results):
                     bad.append((w, ins))
     return bad
 
@@ -113,6 +115,7 @@ def test_the_checks_see_a_missing_wait():
     assert check_scalars(["v_readlane_b32 s6, v9, 3", "s_mov_b32 m0, s3", "s_nop 2", load])
     assert not check_scalars(["v_readlane_b32 s6, v9, 3", "s_mov_b32 m0, s3", "s_nop 4", load])
     assert not check_scalars(["v_readlane_b32 s8, v9, 3", load])
+    assert check_scalars(["v_add_co_u32_e64 v0, s[4:5], v1, v2", load])
 
 
 def test_lds_loads_wait_for_m0(listings):
