@@ -28,6 +28,9 @@ GPTQ_GRID_ASYMMETRIC = 1
 GPTQ_MX_E2M1 = 0  # MX elements of 4 bits
 GPTQ_MX_E4M3 = 1  # MX elements of 8 bits
 
+GPTQ_NORM_INT8 = 0  # the norm's output: integers with a scale a row
+GPTQ_NORM_E4M3 = 1  # or MX blocks
+
 # every symbol the headers declare, with its ctypes signature
 _c_int64 = ctypes.c_int64
 _vp = ctypes.c_void_p
@@ -76,6 +79,22 @@ SIGNATURES = {
     "gptq_mx_grad_weight_workspace_bytes": (ctypes.c_size_t, [_c_int64, _c_int64, _c_int64]),
     "gptq_mx_grad_weight": (ctypes.c_int, [_vp, _c_int64, _c_int64, _c_int64, _vp, _vp, ctypes.c_int, _c_int64,
                                            ctypes.c_int, _vp, ctypes.c_int, _c_int64, _vp, _vp, ctypes.c_size_t, _vp]),
+    "gptq_int8_code_bytes_per_row": (_c_int64, [_c_int64]),
+    "gptq_int8_quantize": (ctypes.c_int, [_vp, ctypes.c_int, _c_int64, _c_int64, _c_int64, _vp, _vp, _vp]),
+    "gptq_int8_dequantize": (ctypes.c_int, [_vp, _vp, _c_int64, _c_int64, _vp, ctypes.c_int, _c_int64, _vp]),
+    "gptq_int8_pad_codes": (ctypes.c_int, [_vp, _c_int64, _c_int64, _vp, _vp]),
+    "gptq_int8_matmul_workspace_bytes": (ctypes.c_size_t, [_c_int64, _c_int64, _c_int64]),
+    "gptq_int8_matmul": (ctypes.c_int, [_vp, _vp, _c_int64, _c_int64, _vp, _vp, _c_int64, _vp, ctypes.c_int, _vp,
+                                        ctypes.c_int, _c_int64, _vp, ctypes.c_size_t, _vp]),
+    "gptq_int8_linear_workspace_bytes": (ctypes.c_size_t, [_c_int64, _c_int64, _c_int64]),
+    "gptq_int8_linear": (ctypes.c_int, [_vp, ctypes.c_int, _c_int64, _c_int64, _c_int64, _vp, _vp, _c_int64, _vp,
+                                        ctypes.c_int, _vp, ctypes.c_int, _c_int64, _vp, ctypes.c_size_t, _vp]),
+    "gptq_rms_norm": (ctypes.c_int, [_vp, ctypes.c_int, _c_int64, _vp, ctypes.c_int, _c_int64, _c_int64, _c_int64, _vp,
+                                     ctypes.c_double, _vp, _c_int64, ctypes.c_int, _vp, _vp, _vp, _vp]),
+    "gptq_rms_norm_grad_workspace_bytes": (ctypes.c_size_t, [_c_int64, _c_int64]),
+    "gptq_rms_norm_grad": (ctypes.c_int, [_vp, ctypes.c_int, _c_int64, _vp, ctypes.c_int, _c_int64, _vp, _vp, _vp, _c_int64,
+                                          _c_int64, _c_int64, ctypes.c_int, _vp, _c_int64, _vp, _vp, ctypes.c_size_t,
+                                          _vp]),
 }
 
 _lib = None

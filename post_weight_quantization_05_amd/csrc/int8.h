@@ -1,0 +1,63 @@
+// Shared definitions of the 8-bit integer operators and the norm.
+#pragma once
+
+#include "../../include/gptq_mi355x_int8.h"
+#include "mx.h"
+
+namespace gptq {
+
+static inline int64_t int8_code_row(int64_t cols) { return ceil_div(cols, 128) * 128; }
+
+// One operand: rows of codes at their fixed row length, a scale for each.
+struct Int8Matrix {
+  const int8_t* codes;
+  const float* scales;
+  int64_t rows, cols;
+};
+
+// int8_quant.hip
+hipError_t int8_quantize_launch(const void* X, int x_dtype, int64_t n, int64_t in, int64_t ld_x, int8_t* codes,
+                                float* scales, hipStream_t stream);
+hipError_t int8_dequantize_launch(const Int8Matrix& q, void* Y, int y_dtype, int64_t ld_y, hipStream_t stream);
+hipError_t int8_pad_launch(const int8_t* codes, int64_t out, int64_t in, int8_t* padded, hipStream_t stream);
+
+// int8_gemm.hip: Y = A W^T (+ bias) (ReLU)
+size_t int8_matmul_ws_bytes(int64_t n, int64_t in, int64_t out);
+hipError_t int8_matmul_launch(const Int8Matrix& a, const Int8Matrix& w, const float* bias, int relu, void* Y, int y_dtype,
+                              int64_t ld_y, void* ws, hipStream_t stream);
+size_t int8_linear_ws_bytes(int64_t n, int64_t in, int64_t out);
+hipError_t int8_linear_launch(const void* X, int x_dtype, int64_t n, int64_t ld_x, const Int8Matrix& w, const float* bias,
+                              int relu, void* Y, int y_dtype, int64_t ld_y, void* ws, hipStream_t stream);
+
+// norm.hip
+struct NormArgs {
+  const void *x, *r;
+  int64_t ldx, ldr, n;
+  int d;
+  const float* weight;
+  double eps;
+  void* h;
+  int64_t ldh;
+  uint8_t* codes;
+  void* scales;
+  float* rstd;
+};
+hipError_t rms_norm_launch(const NormArgs& a, int x_dtype, int r_dtype, int fmt, hipStream_t stream);
+
+struct NormGradArgs {
+  const void *dy, *h, *dh;
+  int64_t ldy, ldh, lddh, n;
+  int d;
+  const float *rstd, *weight;
+  void* dx;
+  int64_t lddx;
+  int accumulate;
+  float* dweight;
+  double* part;  // rows of d partial sums of dweight
+};
+size_t rms_norm_grad_ws_bytes(int64_t n, int64_t d);
+hipError_t rms_norm_grad_launch(const NormGradArgs& a, int y_dtype, int h_dtype, hipStream_t stream);
+
+typedef __attribute__((ext_vector_type(16))) int i32x16;
+
+}  // namespace gptq

@@ -1,0 +1,86 @@
+// A row's 8-bit integer codes and scale, a lane holding 8 consecutive columns.
+#pragma once
+
+#include "int8.h"
+#include "mx_codec.h"
+
+namespace gptq {
+
+// largest magnitude's fp32 bits (infinities and NaN above every finite value) -> the row's scale
+__device__ __forceinline__ float int8_scale(uint32_t top) {
+  if (top >= 0x7F800000u) return __uint_as_float(0x7FC00000u);
+  return fmaxf(__uint_as_float(top), 1e-12f) / 127.f;
+}
+
+// 8 codes of v / s, the exact quotient rounded to nearest, ties to even; s is finite, |v| <= 127 s (1 + 2^-23), inv is 1 / s
+// to 2 ulp. Adding 1.5 * 2^23 rounds v inv to a whole number, which then stands in the sum's low byte. v inv is off by less
+// than 1e-4, so only a value that close to a tie can have been rounded wrongly: there v - code * s, which one fused
+// multiply-add gives exactly (a multiple of ulp(s) / 2 of at most 24 bits), is compared with s / 2.
+__device__ __forceinline__ uint2 int8_encode(const float (&v)[8], float s, float inv) {
+  constexpr float MAGIC = 12582912.f;
+  float f[8], worst = 0.f;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    f[q] = fmaf(v[q], inv, MAGIC);
+    worst = fmaxf(worst, fabsf(fmaf(v[q], inv, MAGIC - f[q])));
+  }
+  if (worst > 0.4999f) {
+    const float half = 0.5f * s;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const float k = f[q] - MAGIC, e = fmaf(-k, s, v[q]);
+      const bool odd = __float_as_uint(f[q]) & 1u;
+      if (e > half || (odd && e == half)) f[q] += 1.f;
+      else if (e < -half || (odd && e == -half)) f[q] -= 1.f;
+    }
+  }
+  uint32_t w[2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const uint32_t lo = __builtin_amdgcn_perm(__float_as_uint(f[4 * q + 1]), __float_as_uint(f[4 * q]), 0x0C0C0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(__float_as_uint(f[4 * q + 3]), __float_as_uint(f[4 * q + 2]), 0x0C0C0400u);
+    w[q] = lo | hi << 16;
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+__device__ __forceinline__ void store8(void* Y, bool bf16, int64_t off, int c, int d, const float (&y)[8]) {
+  if (bf16) {
+    uint16_t* p = static_cast<uint16_t*>(Y) + off;
+    if (c + 8 <= d) {
+      *reinterpret_cast<i32x4_any*>(p) = (i32x4){(int)bf16_pair(y[0], y[1]), (int)bf16_pair(y[2], y[3]),
+                                                 (int)bf16_pair(y[4], y[5]), (int)bf16_pair(y[6], y[7])};
+    } else {
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (c + q < d) p[q] = (uint16_t)bf16_bits(y[q]);
+    }
+  } else {
+    float* p = static_cast<float*>(Y) + off;
+    if (c + 8 <= d) {
+      reinterpret_cast<f32x4_any*>(p)[0] = (f32x4){y[0], y[1], y[2], y[3]};
+      reinterpret_cast<f32x4_any*>(p)[1] = (f32x4){y[4], y[5], y[6], y[7]};
+    } else {
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (c + q < d) p[q] = y[q];
+    }
+  }
+}
+
+// 8 columns of fp32 numbers from c on, zeros behind the last
+__device__ __forceinline__ void load8(const float* p, int c, int d, float (&v)[8]) {
+  if (c + 8 <= d) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const f32x4 t = reinterpret_cast<const f32x4_any*>(p + c)[q];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[4 * q + e] = t[e];
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] = c + q < d ? p[c + q] : 0.f;
+  }
+}
+
+}  // namespace gptq
