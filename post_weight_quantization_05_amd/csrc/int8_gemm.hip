@@ -1,66 +1,282 @@
 // Y = A W^T s_a s_w (+ bias) (ReLU) with A (n x in) and W (out x in) in 8-bit integers, on v_mfma_i32_32x32x32_i8: sums are
-// whole numbers of at most 128^2 x 65536 = 2^30 and exact in 32 bits.
+// whole numbers of at most 128^2 x 65536 = 2^30 and exact in 32 bits, in any order, so slices of k change no result.
 //
 // W is the first operand, so that a lane of the result holds four consecutive columns of Y. Lane l of an operand holds row
-// l % 32, columns 16 (l / 32) .. + 15 of the 32.
+// l % 32, columns 16 (l / 32) .. + 15 of the 32 (any order of k would do, both operands having the same).
 #include <algorithm>
 
 #include "int8.h"
+#include "mx_tile.h"
 
 namespace gptq {
 
 namespace {
+
+typedef __attribute__((ext_vector_type(4))) unsigned int u32x4;
 
 struct MatmulArgs {
   const int8_t *ac, *wc;
   const float *as, *ws, *bias;
   void* Y;
   int64_t n, ld;
-  int kp, out, relu;
+  int kp;            // bytes of a row of codes
+  int out, ta, tb;   // tiles along out and along tokens
+  int nk, slice;     // 128s of columns; those of a slice
+  int relu;
 };
 
-// a workgroup forms 64 x 64, each wave 32 x 32, operands straight from memory
-template <bool YBF16>
-__global__ __launch_bounds__(256) void k_int8_matmul(const MatmulArgs g) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 31, h = lane >> 5;
-  const int64_t row = (int64_t)blockIdx.y * 64 + (wave >> 1) * 32 + r;
-  const int o0 = blockIdx.x * 64 + (wave & 1) * 32;
-  const int8_t* a = g.ac + min(row, g.n - 1) * g.kp + 16 * h;
-  const int8_t* w = g.wc + (int64_t)min(o0 + r, g.out - 1) * g.kp + 16 * h;
-  i32x16 acc = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-  for (int k = 0; k < g.kp; k += 32)
-    acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(*reinterpret_cast<const i32x4*>(w + k), *reinterpret_cast<const i32x4*>(a + k),
-                                                acc, 0, 0, 0);
-  if (row >= g.n) return;
-  const float s = g.as[row];
+// What a wave needs of the scales and the bias for its results, 32 MB columns by 32 NB rows: they come by transfers to LDS
+// before the products and into registers behind them, a lane holding every 64th. (Loaded between the stores they
+// would wait for them, and before them for memory: with both, 16384 x 4096 x 11008 took 97 us for its results instead of XX.)
+template <int MB, int NB>
+struct WaveScales {
+  static constexpr int NC = (32 * MB + 63) / 64, NR = (32 * NB + 63) / 64;
+  static constexpr int BYTES = (2 * NC + NR) * 256, TRANSFERS = 2 * NC + NR;
+  float w[NC], b[NC], s[NR];
+
+  static __device__ __forceinline__ i32x4 buffer(const float* p, int64_t count) {
+    const uint64_t a = (uint64_t)uniform64((int64_t)(uintptr_t)p);
+    const int n = p && count > 0 ? (int)min(count, (int64_t)256) * 4 : 0;  // outside: zeros
+    return (i32x4){(int)(uint32_t)a, (int)(uint32_t)(a >> 32) & 0xFFFF, __builtin_amdgcn_readfirstlane(n), 0x00020000};
+  }
+  static __device__ __forceinline__ void fetch(const MatmulArgs& g, uint32_t at, int c0, int64_t row0) {
+    const uint32_t off = (threadIdx.x & 63) * 4;
+    const i32x4 w = buffer(g.ws + c0, g.out - c0), b = buffer(g.bias ? g.bias + c0 : nullptr, g.out - c0);
+    const i32x4 s = buffer(g.as + row0, g.n - row0);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int c = o0 + 8 * (i / 4) + 4 * h + i % 4;
-    if (c >= g.out) continue;
-    float y = (float)acc[i] * s * g.ws[c];
-    if (g.bias) y += g.bias[c];
-    if (g.relu) y = relu_nan(y);
+    for (int i = 0; i < NC; ++i) {
+      dma4(w, (uint32_t)__builtin_amdgcn_readfirstlane((int)(at + i * 256)), off + i * 256);
+      dma4(b, (uint32_t)__builtin_amdgcn_readfirstlane((int)(at + (NC + i) * 256)), off + i * 256);
+    }
+#pragma unroll
+    for (int i = 0; i < NR; ++i) dma4(s, (uint32_t)__builtin_amdgcn_readfirstlane((int)(at + (2 * NC + i) * 256)), off + i * 256);
+  }
+  __device__ __forceinline__ void take(const uint8_t* at) {
+    const float* p = reinterpret_cast<const float*>(at) + (threadIdx.x & 63);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) w[i] = p[i * 64], b[i] = p[(NC + i) * 64];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) s[i] = p[(2 * NC + i) * 64];
+  }
+  // entry i of a row of them, i / 64 the same in all lanes
+  template <int N>
+  static __device__ __forceinline__ float pick(const float (&v)[N], int part, int lane) {
+    return __int_as_float(__builtin_amdgcn_ds_bpermute(lane * 4, __float_as_int(v[part])));
+  }
+};
+
+// Writes a wave's results: register i of lane l of acc[mb][nb] is row 32 nb + l % 32, column 32 mb + 8 (i / 4) + 4 (l / 32) + i % 4.
+// The sums go through LDS, 32 PB columns of 32 rows at a time, so that a store takes runs of 128 bytes of a row or more; they
+// leave past the caches' reuse (nontemporal: 643 against 659 us at 16384 x 4096 x 11008). Returns the stores that
+// a wave inside Y has issued, 0 at an edge. RAW: the sums themselves, to partial results.
+template <bool YBF16, bool RAW, int PB, int MB, int NB>
+__device__ __forceinline__ int store_int8(const f32x16 (&acc)[MB][NB], uint8_t* lds, const WaveScales<MB, NB>& sc,
+                                          const MatmulArgs& g, void* __restrict__ Y, int64_t ld, int64_t row0, int c0) {
+  constexpr int C = 32 * PB, V = YBF16 ? 8 : 4, PER_ROW = C / V, STEP = 64 / PER_ROW, IT = 32 / STEP;
+  const int lane = threadIdx.x & 63;
+  int* buf = reinterpret_cast<int*>(lds);
+  const int r = lane & 31, h = lane >> 5;
+  constexpr int ES = YBF16 ? 2 : 4;
+  const bool inside = row0 + 32 * NB <= g.n && c0 + 32 * MB <= g.out && ld < (int64_t)1 << 22;
+  const __amdgpu_buffer_rsrc_t to = __builtin_amdgcn_make_buffer_rsrc(
+      static_cast<uint8_t*>(Y) + uniform64((row0 * ld + c0) * ES), 0, 0x7FFFFFF0, 0x00020000);
+  const int step = __builtin_amdgcn_readfirstlane((int)ld * ES);  // used inside only
+  const int first = (lane / PER_ROW) * step + (lane % PER_ROW) * 16;
+  const float low = g.relu ? 0.f : -__builtin_inff();
+  // the 16-byte chunks of row r are permuted by XOR with r, so that neither side's rows meet on the same banks
+  auto chunk = [](int row, int q) { return row * C + ((q ^ (row & (C / 4 - 1))) << 2); };
+#pragma unroll
+  for (int m0 = 0; m0 < MB; m0 += PB) {
+    float w[V], b[V];
+    if (!RAW) {
+#pragma unroll
+      for (int q = 0; q < V; ++q) {
+        const int at = m0 % 2 * 32 + (lane % PER_ROW) * V + q;
+        w[q] = sc.pick(sc.w, m0 / 2, at), b[q] = sc.pick(sc.b, m0 / 2, at);
+      }
+    }
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      float s[IT];
+#pragma unroll
+      for (int it = 0; it < IT; ++it) s[it] = RAW ? 0.f : sc.pick(sc.s, nb / 2, nb % 2 * 32 + lane / PER_ROW + it * STEP);
+#pragma unroll
+      for (int mb = 0; mb < PB; ++mb)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<float4*>(buf + chunk(r, mb * 8 + 2 * q + h)) =
+              make_float4(acc[m0 + mb][nb][4 * q], acc[m0 + mb][nb][4 * q + 1], acc[m0 + mb][nb][4 * q + 2],
+                          acc[m0 + mb][nb][4 * q + 3]);
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int it = 0; it < IT; ++it) {
+        float v[V];
+#pragma unroll
+        for (int q = 0; q < V / 4; ++q) {
+          const i32x4 x = *reinterpret_cast<const i32x4*>(
+              buf + chunk(lane / PER_ROW + it * STEP, (lane % PER_ROW) * (V / 4) + q));
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            v[4 * q + e] = RAW ? __int_as_float(x[e]) : int8_result((float)x[e], s[it], w[4 * q + e], b[4 * q + e], low);
+        }
+        if (inside) {
+          i32x4 o;
+          if (YBF16)
+            o = (i32x4){(int)bf16_pair(v[0], v[1]), (int)bf16_pair(v[2], v[3]), (int)bf16_pair(v[V - 4], v[V - 3]),
+                        (int)bf16_pair(v[V - 2], v[V - 1])};
+          else
+            o = __builtin_bit_cast(i32x4, (f32x4){v[0], v[1], v[2], v[3]});
+          // No scalar offset: behind a 16-byte store with one the compiler leaves out the wait state before a vector
+          // instruction that writes its data registers, and here such stores took the new contents now and then.
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o), to,
+                                                 first + ((nb * 32 + it * STEP) * step + 32 * m0 * ES), 0, 2);
+        } else {
+          const int64_t row = row0 + nb * 32 + lane / PER_ROW + it * STEP;
+          const int c = c0 + 32 * m0 + (lane % PER_ROW) * V, n = row < g.n ? g.out - c : 0;
+#pragma unroll
+          for (int q = 0; q < V; ++q) {
+            if (q >= n) continue;
+            if (YBF16) static_cast<uint16_t*>(Y)[row * ld + c + q] = (uint16_t)bf16_bits(v[q]);
+            else static_cast<float*>(Y)[row * ld + c + q] = v[q];
+          }
+        }
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
+  }
+  return inside ? 1 : 0;
+}
+
+template <bool YBF16, int WA, int WB, int MB, int NB, int OCC>
+__global__ __launch_bounds__(256, OCC) void k_int8_matmul(const MatmulArgs g) {
+  using T = TileProduct<K_INT8, K_INT8, WA, WB, MB, NB>;
+  using S = WaveScales<MB, NB>;
+  constexpr int PB = MB >= 2 ? 2 : 1;
+  // results pass through memory of their own (large tiles) or the ring's; the scales wait in the former or behind the ring
+  constexpr int RESULTS = T::STAYS ? T::LDS - 4 * 4096 * PB : 0, SCALES = T::STAYS ? RESULTS : T::LDS;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[T::STAYS ? T::LDS : T::LDS + 4 * S::BYTES];
+  TileOrder order;
+  order.init(blockIdx.x, gridDim.x, g.ta, g.tb);
+  int ia, ib;
+  if (!order.get(0, ia, ib)) return;
+  const int k0 = blockIdx.y * g.slice, stages = min(g.slice, g.nk - k0);
+  T t;
+  t.init(lds, 0);
+  t.a.init(g.kp, t.wave, t.lane, t.wa);
+  t.b.init(g.kp, t.wave, t.lane, t.wb);
+  t.tail = 0;
+  uint8_t* results = lds + RESULTS + t.wave * (4096 * PB);
+  const int scales = SCALES + t.wave * (T::STAYS ? 4096 * PB : S::BYTES);
+  auto locate = [&](bool any, Stretch& a, Stretch& b) {
+    const int o0 = ia * WA, n = any ? stages : 0;
+    const int64_t t0 = (int64_t)ib * WB, kb = (int64_t)k0 * 128;
+    a.init(g.wc + (int64_t)o0 * g.kp + kb, (int64_t)min(WA, g.out - o0) * g.kp - kb, T::A::STEP, n);
+    b.init(g.ac + t0 * g.kp + kb, min((int64_t)WB, g.n - t0) * g.kp - kb, T::B::STEP, n);
+  };
+  locate(true, t.a.mem, t.b.mem);
+  t.start();
+  bool more = true;
+  int stored = 0;
+  for (int r = 1; more; ++r) {
+    const int64_t row0 = (int64_t)ib * WB + t.wb;
+    const int c0 = ia * WA + t.wa;
+    more = order.get(r, ia, ib);
+    locate(more, t.an, t.bn);
+    S::fetch(g, t.base + scales, c0, row0);
+    constexpr int STORES = MB / PB * NB * (YBF16 ? 4 * PB / 2 : 4 * PB);
+    t.template multiply<STORES>(max(2, stages), __builtin_amdgcn_readfirstlane(stored));
+    if (!T::STAYS) wait_and_barrier<0>();
+    S sc;
+    sc.take(lds + scales);
+    if (gridDim.y > 1) {
+      float* part = static_cast<float*>(g.Y) + blockIdx.y * g.n * (int64_t)g.out;
+      store_int8<false, true, PB>(t.acc, results, sc, g, part, g.ld, row0, c0);
+      stored = 0;
+    } else {
+      stored = store_int8<YBF16, false, PB>(t.acc, results, sc, g, g.Y, g.ld, row0, c0);
+    }
+    if (!T::STAYS) return;
+    t.clear();
+  }
+  wait_and_barrier<0>();  // nothing may still be writing LDS when the workgroup ends
+}
+
+// The slices' partial sums added; scales, bias, ReLU and the result's type.
+template <bool YBF16>
+__global__ __launch_bounds__(256) void k_int8_join(const MatmulArgs g, const int* __restrict__ part, int slices) {
+  const int64_t total = g.n * g.out;
+  const float low = g.relu ? 0.f : -__builtin_inff();
+  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += (int64_t)gridDim.x * 256) {
+    int sum = 0;
+    for (int s = 0; s < slices; ++s) sum += part[s * total + e];
+    const int64_t row = e / g.out;
+    const int c = (int)(e - row * g.out);
+    const float y = int8_result((float)sum, g.as[row], g.ws[c], g.bias ? g.bias[c] : 0.f, low);
     if (YBF16) static_cast<uint16_t*>(g.Y)[row * g.ld + c] = (uint16_t)bf16_bits(y);
     else static_cast<float*>(g.Y)[row * g.ld + c] = y;
   }
 }
 
+struct MatmulPlan {
+  int tile;    // 64 << tile, along out and along tokens
+  int slices;  // of k
+};
+
+MatmulPlan matmul_plan(int64_t n, int64_t in, int64_t out) {
+  const int64_t nk = ceil_div(in, 128);
+  auto tiles = [&](int64_t w) { return ceil_div(out, w) * ceil_div(n, w); };
+  MatmulPlan p = {0, 1};
+  if (tiles(256) >= 192 && nk >= 8) p.tile = 2;
+  else if (tiles(128) >= 224) p.tile = 1;
+  if (const char* e = getenv("I8_TILE")) p.tile = atoi(e);
+  const int64_t t = tiles(64 << p.tile);
+  if (t > 0 && t < 256) p.slices = (int)std::max<int64_t>(1, std::min<int64_t>({256 / t, nk / 24, 16}));
+  if (const char* e = getenv("I8_SLICES")) p.slices = atoi(e);
+  return p;
+}
+
+template <bool YBF16>
+void matmul_go(int tile, dim3 grid, hipStream_t stream, const MatmulArgs& g) {
+#define GPTQ_GO(W, B, OCC) hipLaunchKernelGGL((k_int8_matmul<YBF16, W, W, B, B, OCC>), grid, dim3(256), 0, stream, g)
+  if (tile == 2) GPTQ_GO(256, 4, 1);
+  else if (tile == 1) GPTQ_GO(128, 2, 2);
+  else GPTQ_GO(64, 1, 3);
+#undef GPTQ_GO
+}
+
 }  // namespace
 
-size_t int8_matmul_ws_bytes(int64_t n, int64_t in, int64_t out) { return 0; }
+size_t int8_matmul_ws_bytes(int64_t n, int64_t in, int64_t out) {
+  const MatmulPlan p = matmul_plan(n, in, out);
+  return p.slices > 1 ? align_up((size_t)p.slices * n * out * 4, 256) : 0;
+}
 
 hipError_t int8_matmul_launch(const Int8Matrix& a, const Int8Matrix& w, const float* bias, int relu, void* Y, int y_dtype,
                               int64_t ld_y, void* ws, hipStream_t stream) {
+  const MatmulPlan p = matmul_plan(a.rows, a.cols, w.rows);
+  const bool bf16 = y_dtype == GPTQ_BF16;
   MatmulArgs g = {};
   g.kp = (int)int8_code_row(a.cols);
-  g.wc = w.codes, g.ws = w.scales, g.bias = bias, g.ld = ld_y, g.out = (int)w.rows, g.relu = relu;
-  constexpr int64_t ROWS_MAX = 64 * 256;
-  for (int64_t r = 0; r < a.rows; r += ROWS_MAX) {
-    g.n = std::min(ROWS_MAX, a.rows - r);
+  g.wc = w.codes, g.ws = w.scales, g.bias = bias, g.out = (int)w.rows, g.relu = relu;
+  g.ta = (int)ceil_div(w.rows, 64 << p.tile), g.nk = (int)ceil_div(a.cols, 128);
+  g.slice = (int)ceil_div(g.nk, p.slices);
+  const int slices = (int)ceil_div(g.nk, g.slice);
+  // at most 2^20 tiles a launch
+  const int64_t rows_max = p.slices > 1 ? a.rows : std::max<int64_t>(1, ((int64_t)1 << 20) / g.ta) * (64 << p.tile);
+  for (int64_t r = 0; r < a.rows; r += rows_max) {
+    g.n = std::min(rows_max, a.rows - r);
+    g.tb = (int)ceil_div(g.n, 64 << p.tile);
     g.ac = a.codes + r * g.kp, g.as = a.scales + r;
-    g.Y = static_cast<uint8_t*>(Y) + r * ld_y * (y_dtype == GPTQ_BF16 ? 2 : 4);
-    const dim3 grid((unsigned)ceil_div(w.rows, 64), (unsigned)ceil_div(g.n, 64));
-    hipLaunchKernelGGL(y_dtype == GPTQ_BF16 ? k_int8_matmul<true> : k_int8_matmul<false>, grid, dim3(256), 0, stream, g);
+    g.Y = static_cast<uint8_t*>(Y) + r * ld_y * (bf16 ? 2 : 4), g.ld = ld_y;
+    if (slices > 1) g.Y = ws, g.ld = w.rows;
+    const dim3 grid(tile_grid((int64_t)g.ta * g.tb, p.tile == 2 ? 256 : 1 << 30), (unsigned)slices);
+    bf16 ? matmul_go<true>(p.tile, grid, stream, g) : matmul_go<false>(p.tile, grid, stream, g);
+  }
+  if (slices > 1) {
+    g.Y = Y, g.ld = ld_y;
+    const dim3 grid((unsigned)std::min<int64_t>(2048, ceil_div(a.rows * w.rows, 256)));
+    hipLaunchKernelGGL(bf16 ? k_int8_join<true> : k_int8_join<false>, grid, dim3(256), 0, stream, g,
+                       static_cast<const int*>(ws), slices);
   }
   return hipGetLastError();
 }

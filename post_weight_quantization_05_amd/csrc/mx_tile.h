@@ -1,4 +1,4 @@
-// The tile product that the MX operators' large kernels share: a workgroup of four waves forms WA x WB of the sum over
+// The tile product that the large kernels of the MX and the 8-bit integer operators share: a workgroup of four waves forms WA x WB of the sum over
 // k of a(i, k) b(j, k), operands streaming from memory straight into a ring of LDS stages while the matrix cores work
 // on earlier ones.
 //
@@ -9,12 +9,12 @@
 // for: a stage therefore takes whole lines, 128 bytes of each row (64 bytes of each row, twice, cost 2.5 times the
 // lines of the 4-bit product at 16384 x 4096 x 11008 with its scales, 16 TB/s, which was the limit).
 //
-// A stage holds four steps of k (64 columns each for MX, 16 for bf16), two stages make the ring. The fragments of a step
+// A stage holds four steps of k (64 columns each for MX, 16 for bf16, 32 for int8), two stages make the ring. The fragments of a step
 // are read between the products of the step before. Before the last step of a stage its buffer has been read by all
 // waves and the next stage has arrived (one wait, one barrier); between its products go the first fragments of the next
 // stage and the transfers of the stage after that, which have until the next such point to land.
 //
-// Stage layout. Operands whose k runs along a row (E2M1, E4M3, bf16) keep 128 bytes of each row together (E4M3: two such
+// Stage layout. Operands whose k runs along a row (E2M1, E4M3, bf16, int8) keep 128 bytes of each row together (E4M3: two such
 // planes); the 16-byte chunks of row r are permuted by XOR with the Gray code of r, so that the consecutive rows that
 // one ds_read_b128 takes at one logical chunk lie on different banks. Operands whose k runs down the columns (bf16, "T")
 // keep each k's row together and are read by the transposing ds_read_b64_tr_b16; chunks are permuted by bits of k.
@@ -26,7 +26,7 @@
 
 namespace gptq {
 
-enum { K_E2M1 = 0, K_E4M3 = 1, K_BF16 = 2, K_BF16T = 3 };
+enum { K_E2M1 = 0, K_E4M3 = 1, K_BF16 = 2, K_BF16T = 3, K_INT8 = 4 };
 
 
 template <int I, int N, typename F>
@@ -52,7 +52,14 @@ __device__ __forceinline__ void dma16(const i32x4& rsrc, uint32_t lds_addr, uint
                : "s"(lds_addr), "v"(voff), "s"(rsrc)
                : "memory", "m0");
 }
-// the same where `skip` is 0; a branch of the compiler's would let it move products across the ring's barriers
+// 64 lanes x 4 B, for what is only 4-byte aligned
+__device__ __forceinline__ void dma4(const i32x4& rsrc, uint32_t lds_addr, uint32_t voff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+               :
+               : "s"(lds_addr), "v"(voff), "s"(rsrc)
+               : "memory", "m0");
+}
+// dma16 where `skip` is 0; a branch of the compiler's would let it move products across the ring's barriers
 __device__ __forceinline__ void dma16_unless(int skip, const i32x4& rsrc, uint32_t lds_addr, uint32_t voff) {
   asm volatile("s_cmp_lg_u32 %3, 0\n\ts_cbranch_scc1 .Lno_transfer%=\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\t"
                "buffer_load_dwordx4 %1, %2, 0 offen lds\n.Lno_transfer%=:"
@@ -67,6 +74,17 @@ template <int N>
 __device__ __forceinline__ void wait_and_barrier() {
   static_assert(N >= 0 && N < 64, "vmcnt range");
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
+}
+
+// the same with at most M in flight where `more` is not 0
+template <int N, int M>
+__device__ __forceinline__ void wait_and_barrier_or(int more) {
+  static_assert(N >= 0 && N < 64 && M >= 0 && M < 64, "vmcnt range");
+  asm volatile("s_cmp_lg_u32 %0, 0\n\ts_cbranch_scc1 .Lmore%=\n\ts_waitcnt vmcnt(%1)\n.Lmore%=:\n\t"
+               "s_waitcnt vmcnt(%2) lgkmcnt(0)\n\ts_barrier"
+               :
+               : "s"(more), "n"(N), "n"(M)
+               : "memory", "scc");
 }
 
 __device__ __forceinline__ int64_t uniform64(int64_t v) {
@@ -196,7 +214,8 @@ __device__ __forceinline__ i32x8 as_operand(const int (&f)[N]) {
   return v;
 }
 
-// A (first operand) x B (second): KA is K_E2M1 with KB K_E2M1 or K_E4M3, or both are bf16 kinds.
+// A (first operand) x B (second): KA is K_E2M1 with KB K_E2M1 or K_E4M3, or both are bf16 kinds, or both K_INT8 (whose
+// sums are whole numbers in 32 bits, kept as the bits of acc).
 // E4M3 fragments are multiplied in two parts (see split_e4m3).
 template <int KA, int KB, int WA, int WB, int MB, int NB>
 struct TileProduct {
@@ -221,6 +240,18 @@ struct TileProduct {
   // and second. All of them between the last step's products saturate the L1's 64 bytes a cycle while the matrix cores
   // wait (16384 x 4096 x 11008 in 4 bits: 478 us, against 444); spread over all four steps the last ones arrive late (455).
   static constexpr int D3 = PER * 8 / 16, D0 = PER * 12 / 16, D1 = PER;
+  // Large int8 tiles hold the fragments of all four steps: those of the next stage's first three are read during the last
+  // step and those of its fourth during its own first, so that a buffer is free for the stage after next from a stage's second
+  // step on. Transfers then have up to six steps to land instead of four; shares as above, in the second, third and fourth
+  // step. us for 16384 x 4096 x 11008 with the shares of two steps' fragments 717, with these 672 (4, 8, 12 of 16: 665, 8, 16,
+  // 16: 667; all in the second step: 681).
+  static constexpr bool DEEP = KA == K_INT8 && MB == 4;
+  static constexpr int SETS = DEEP ? 4 : 2;
+#ifndef I8C1
+#define I8C1 6
+#define I8C2 11
+#endif
+  static constexpr int C1 = PER * I8C1 / 16, C2 = PER * I8C2 / 16;
   static_assert(!MX || (WA % 64 == 0 && WB % 64 == 0), "scale transfers");
 
   A a;
@@ -235,7 +266,7 @@ struct TileProduct {
   uint32_t svoff[SI ? SI : 1], soff;
   int stile[SI ? SI : 1];
   f32x16 acc[MB][NB];
-  int fa[2][MB][A::FRAG], fb[2][NB][B::FRAG];
+  int fa[SETS][MB][A::FRAG], fb[SETS][NB][B::FRAG];
   int sca[MB][2], scb[NB][2], nca[MB][4], ncb[NB][4];
 
   __device__ __forceinline__ void init(uint8_t* l, int64_t srow) {
@@ -317,7 +348,12 @@ struct TileProduct {
 
   template <int SET, int J, int M, int N>
   __device__ __forceinline__ void product() {
-    if constexpr (!MX) {
+    if constexpr (KA == K_INT8) {
+      acc[M][N] = __builtin_bit_cast(f32x16, __builtin_amdgcn_mfma_i32_32x32x32_i8(
+          (i32x4){fa[SET][M][0], fa[SET][M][1], fa[SET][M][2], fa[SET][M][3]},
+          (i32x4){fb[SET][N][0], fb[SET][N][1], fb[SET][N][2], fb[SET][N][3]}, __builtin_bit_cast(i32x16, acc[M][N]), 0,
+          0, 0));
+    } else if constexpr (!MX) {
       acc[M][N] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
           __builtin_bit_cast(bf16x8, (i32x4){fa[SET][M][0], fa[SET][M][1], fa[SET][M][2], fa[SET][M][3]}),
           __builtin_bit_cast(bf16x8, (i32x4){fb[SET][N][0], fb[SET][N][1], fb[SET][N][2], fb[SET][N][3]}), acc[M][N],
@@ -348,6 +384,37 @@ struct TileProduct {
       static_for<T0 + i * (T1 - T0) / NM, T0 + (i + 1) * (T1 - T0) / NM>([&](auto t) { transfer(decltype(t)::value, to); });
       __builtin_amdgcn_sched_barrier(0);
     });
+  }
+
+  // step J with fragments R0 .. R1 - 1 of a stage (in order of their steps) and transfers T0 .. T1 - 1 between its products
+  template <int J, int R0, int R1, int T0, int T1>
+  __device__ __forceinline__ void deep_step(uint32_t from, uint32_t to) {
+    static_for<0, NM>([&](auto ic) {
+      constexpr int i = decltype(ic)::value;
+      product<J, J, i / NB, i % NB>();
+      static_for<R0 + i * (R1 - R0) / NM, R0 + (i + 1) * (R1 - R0) / NM>([&](auto t) {
+        constexpr int S = decltype(t)::value / (MB + NB);
+        read_frag<S, S, decltype(t)::value % (MB + NB)>(from);
+      });
+      static_for<T0 + i * (T1 - T0) / NM, T0 + (i + 1) * (T1 - T0) / NM>([&](auto t) { transfer(decltype(t)::value, to); });
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  }
+
+  // behind: transfers and stores (at least) that were issued since the next stage's transfers, or 0 if that is not known
+  template <int BEHIND>
+  __device__ __forceinline__ void deep_stage(int at, int nk, int behind) {
+    constexpr int F = MB + NB;
+    const uint32_t other = STAGE - slot;
+    deep_step<0, 3 * F, 4 * F, 0, 0>(slot, slot);
+    wait_and_barrier<63>();  // all waves have read all of the stage
+    const bool cross = at + 2 == nk;
+    a.mem.take_if(cross, an), b.mem.take_if(cross, bn);
+    deep_step<1, 0, 0, 0, C1>(slot, slot);
+    deep_step<2, 0, 0, C1, C2>(slot, slot);
+    wait_and_barrier_or<C2, (C2 + BEHIND < 63 ? C2 + BEHIND : 63)>(behind);
+    deep_step<3, 0, 3 * F, C2, PER>(other, slot);
+    slot = other;
   }
 
   // stage `at` of nk, the P-th of a pair
@@ -384,19 +451,31 @@ struct TileProduct {
     if constexpr (MX) transfer_scales(0, sa, sb);
 #pragma unroll
     for (int i = 0; i < PER; ++i) transfer(i, 0);
+    constexpr int AHEAD = DEEP ? PER : D3;
 #pragma unroll
-    for (int i = 0; i < D3; ++i) transfer(i, STAGE);
-    wait_and_barrier<D3>();
-    static_for<0, MB + NB>([&](auto t) { read_frag<0, 0, decltype(t)::value>(0); });
+    for (int i = 0; i < AHEAD; ++i) transfer(i, STAGE);
+    wait_and_barrier<AHEAD>();
+    static_for<0, (DEEP ? 3 : 1) * (MB + NB)>([&](auto t) {
+      constexpr int S = decltype(t)::value / (MB + NB);
+      read_frag<S, S, decltype(t)::value % (MB + NB)>(0);
+    });
     if constexpr (MX) read_scales(0);
   }
 
   // A tile; when it ends, the first stages of the next one (an, bn, san, sbn; no stages if there is none) are on their
-  // way.
-  __device__ __forceinline__ void multiply(int nk) {
+  // way. DEEP: behind != 0 says that this wave issued BEHIND loads and stores at least since the multiply before, which the
+  // first stage does not wait for.
+  template <int BEHIND = 0>
+  __device__ __forceinline__ void multiply(int nk, int behind = 0) {
     if constexpr (MX) {
       for (int at = 0; at < nk; at += 2) stage<0>(at, nk), stage<1>(at + 1, nk);
       sa = san, sb = sbn;
+    } else if constexpr (DEEP) {
+      for (int at = 0; at < nk; ++at) {
+        int first = at;
+        asm("" : "+s"(first));  // keeps the compiler from expanding the first stage apart from the others
+        deep_stage<BEHIND>(at, nk, first == 0 ? behind : 0);
+      }
     } else {
       for (int at = 0; at < nk; ++at) stage<0>(at, nk);
     }
