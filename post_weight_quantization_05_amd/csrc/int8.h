@@ -29,6 +29,16 @@ size_t int8_linear_ws_bytes(int64_t n, int64_t in, int64_t out);
 hipError_t int8_linear_launch(const void* X, int x_dtype, int64_t n, int64_t ld_x, const Int8Matrix& w, const float* bias,
                               int relu, void* Y, int y_dtype, int64_t ld_y, void* ws, hipStream_t stream);
 
+// int8_few.hip: the same for at most INT8_FEW tokens, in codes or, where they are small enough, quantized on their way in
+constexpr int INT8_FEW = 16;
+static inline bool int8_few_fused(int64_t n, int64_t in) {
+  return n <= INT8_FEW && in >= 8 && (n <= 2 ? n : n <= 4 ? 4 : n <= 8 ? 8 : 16) * in <= 8 * 4096;
+}
+hipError_t int8_matmul_few_launch(const Int8Matrix& x, const Int8Matrix& w, const float* bias, int relu, void* Y, int y_dtype,
+                                  int64_t ld_y, hipStream_t stream);
+hipError_t int8_linear_few_launch(const void* X, int x_dtype, int64_t n, int64_t ld_x, const Int8Matrix& w, const float* bias,
+                                  int relu, void* Y, int y_dtype, int64_t ld_y, hipStream_t stream);
+
 // norm.hip
 struct NormArgs {
   const void *x, *r;

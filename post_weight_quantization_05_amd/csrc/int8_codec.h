@@ -13,9 +13,10 @@ __device__ __forceinline__ float int8_scale(uint32_t top) {
 }
 
 // 8 codes of v / s, the exact quotient rounded to nearest, ties to even; s is finite, |v| <= 127 s (1 + 2^-23), inv is 1 / s
-// to 2 ulp. Adding 1.5 * 2^23 rounds v inv to a whole number, which then stands in the sum's low byte. v inv is off by less
-// than 1e-4, so only a value that close to a tie can have been rounded wrongly: there v - code * s, which one fused
-// multiply-add gives exactly (a multiple of ulp(s) / 2 of at most 24 bits), is compared with s / 2.
+// to 2 ulp. Adding 1.5 * 2^23 rounds v inv to a whole number k, which then stands in the sum's low byte. v inv is off by less
+// than 1e-4, so only a value that close to a tie can have been rounded wrongly. There e = v - k s, which one fused multiply-add
+// gives exactly (a multiple of ulp(s) / 2 of at most 24 bits), is compared with s / 2: beyond it k is one off, and at it if
+// k is odd. Values in bf16 meet ties often (one in 400 is a tie exactly if the largest one is even), so this way is short too.
 __device__ __forceinline__ uint2 int8_encode(const float (&v)[8], float s, float inv) {
   constexpr float MAGIC = 12582912.f;
   float f[8], worst = 0.f;
@@ -25,13 +26,14 @@ __device__ __forceinline__ uint2 int8_encode(const float (&v)[8], float s, float
     worst = fmaxf(worst, fabsf(fmaf(v[q], inv, MAGIC - f[q])));
   }
   if (worst > 0.4999f) {
-    const float half = 0.5f * s;
+    const uint32_t half = __float_as_uint(0.5f * s);
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      const float k = f[q] - MAGIC, e = fmaf(-k, s, v[q]);
-      const bool odd = __float_as_uint(f[q]) & 1u;
-      if (e > half || (odd && e == half)) f[q] += 1.f;
-      else if (e < -half || (odd && e == -half)) f[q] -= 1.f;
+      const uint32_t k = __float_as_uint(f[q]);
+      const float e = fmaf(MAGIC - f[q], s, v[q]);
+      // |e| > half or |e| == half with k odd, as one comparison of whole numbers
+      const uint32_t off = (__float_as_uint(e) & 0x7FFFFFFFu) + (k & 1u) > half ? 1u : 0u;
+      f[q] = __uint_as_float(k + ((__float_as_uint(e) >> 31) ? 0u - off : off));
     }
   }
   uint32_t w[2];

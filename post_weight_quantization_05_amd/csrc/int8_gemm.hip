@@ -4,6 +4,7 @@
 // W is the first operand, so that a lane of the result holds four consecutive columns of Y. Lane l of an operand holds row
 // l % 32, columns 16 (l / 32) .. + 15 of the 32 (any order of k would do, both operands having the same).
 #include <algorithm>
+#include <cmath>
 
 #include "int8.h"
 #include "mx_tile.h"
@@ -27,7 +28,7 @@ struct MatmulArgs {
 
 // What a wave needs of the scales and the bias for its results, 32 MB columns by 32 NB rows: they come by transfers to LDS
 // before the products and into registers behind them, a lane holding every 64th. (Loaded between the stores they
-// would wait for them, and before them for memory: with both, 16384 x 4096 x 11008 took 97 us for its results instead of XX.)
+// would wait for them, and before them for memory: with both, 16384 x 4096 x 11008 took 97 us of 659 for its results.)
 template <int MB, int NB>
 struct WaveScales {
   static constexpr int NC = (32 * MB + 63) / 64, NR = (32 * NB + 63) / 64;
@@ -147,9 +148,9 @@ __device__ __forceinline__ int store_int8(const f32x16 (&acc)[MB][NB], uint8_t* 
   return inside ? 1 : 0;
 }
 
-template <bool YBF16, int WA, int WB, int MB, int NB, int OCC>
+template <bool YBF16, int WA, int WB, int MB, int NB, int RING, int OCC>
 __global__ __launch_bounds__(256, OCC) void k_int8_matmul(const MatmulArgs g) {
-  using T = TileProduct<K_INT8, K_INT8, WA, WB, MB, NB>;
+  using T = TileProduct<K_INT8, K_INT8, WA, WB, MB, NB, RING>;
   using S = WaveScales<MB, NB>;
   constexpr int PB = MB >= 2 ? 2 : 1;
   // results pass through memory of their own (large tiles) or the ring's; the scales wait in the former or behind the ring
@@ -201,92 +202,143 @@ __global__ __launch_bounds__(256, OCC) void k_int8_matmul(const MatmulArgs g) {
   wait_and_barrier<0>();  // nothing may still be writing LDS when the workgroup ends
 }
 
-// The slices' partial sums added; scales, bias, ReLU and the result's type.
-template <bool YBF16>
+// The slices' partial sums added; scales, bias, ReLU and the result's type. V columns of a row a thread.
+template <bool YBF16, int V>
 __global__ __launch_bounds__(256) void k_int8_join(const MatmulArgs g, const int* __restrict__ part, int slices) {
-  const int64_t total = g.n * g.out;
+  const int per_row = (g.out + V - 1) / V;
+  const int64_t total = g.n * per_row, stride = g.n * g.out;
   const float low = g.relu ? 0.f : -__builtin_inff();
   for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += (int64_t)gridDim.x * 256) {
-    int sum = 0;
-    for (int s = 0; s < slices; ++s) sum += part[s * total + e];
-    const int64_t row = e / g.out;
-    const int c = (int)(e - row * g.out);
-    const float y = int8_result((float)sum, g.as[row], g.ws[c], g.bias ? g.bias[c] : 0.f, low);
-    if (YBF16) static_cast<uint16_t*>(g.Y)[row * g.ld + c] = (uint16_t)bf16_bits(y);
-    else static_cast<float*>(g.Y)[row * g.ld + c] = y;
+    const int64_t row = e / per_row;
+    const int c = (int)(e - row * per_row) * V;
+    const int* p = part + row * g.out + c;
+    int sum[V];
+#pragma unroll
+    for (int q = 0; q < V; ++q) sum[q] = 0;
+#pragma unroll 4
+    for (int s = 0; s < slices; ++s) {
+      if constexpr (V == 4) {
+        const i32x4 v = *reinterpret_cast<const i32x4*>(p + s * stride);
+#pragma unroll
+        for (int q = 0; q < V; ++q) sum[q] += v[q];
+      } else {
+        sum[0] += p[s * stride];
+      }
+    }
+    const float t = g.as[row];
+#pragma unroll
+    for (int q = 0; q < V; ++q) {
+      const float y = int8_result((float)sum[q], t, g.ws[c + q], g.bias ? g.bias[c + q] : 0.f, low);
+      if (YBF16) static_cast<uint16_t*>(g.Y)[row * g.ld + c + q] = (uint16_t)bf16_bits(y);
+      else static_cast<float*>(g.Y)[row * g.ld + c + q] = y;
+    }
   }
 }
 
+// Tiles (along out, along tokens), stages of the ring, and what a round of 256 of them takes, one to a CU: us for 128 columns
+// of k and for the rest. Fitted to 70 sizes from 17 x 102 x 64 to 16384 x 1344 x 11008: times off by 7 to 12 %, and the tile chosen by
+// them 1.4 % slower than the best one on average. The large tiles' rest is mostly that of all results leaving at once.
+struct Tile {
+  int wa, wb, ring;
+  double step, rest;
+};
+constexpr Tile TILES[] = {{64, 64, 4, 0.22, 1.4},   {128, 64, 3, 0.33, 2.0},   {128, 128, 2, 0.50, 3.7}, {128, 128, 4, 0.42, 4.4},
+                          {256, 128, 2, 0.67, 8.2}, {256, 192, 2, 0.86, 12.3}, {256, 256, 2, 1.02, 15.9}};
+
 struct MatmulPlan {
-  int tile;    // 64 << tile, along out and along tokens
+  int tile;    // of TILES
   int slices;  // of k
 };
 
+// The fastest by the times above. Workgroups of tiles that fit a CU together mix their rounds, so those count in parts. Slices
+// of k, joined by another launch of at least 3 us, where few tiles have a long sum each: 64 x 11008 x 4096 takes 17 us with
+// 4 of them and 30 with one, but 200 x 4096 x 4096 (256 tiles of 64) 11 with one and 16 with two.
 MatmulPlan matmul_plan(int64_t n, int64_t in, int64_t out) {
-  const int64_t nk = ceil_div(in, 128);
-  auto tiles = [&](int64_t w) { return ceil_div(out, w) * ceil_div(n, w); };
-  MatmulPlan p = {0, 1};
-  if (tiles(256) >= 192 && nk >= 8) p.tile = 2;
-  else if (tiles(128) >= 224) p.tile = 1;
-  if (const char* e = getenv("I8_TILE")) p.tile = atoi(e);
-  const int64_t t = tiles(64 << p.tile);
-  if (t > 0 && t < 256) p.slices = (int)std::max<int64_t>(1, std::min<int64_t>({256 / t, nk / 24, 16}));
-  if (const char* e = getenv("I8_SLICES")) p.slices = atoi(e);
-  return p;
+  MatmulPlan best = {0, 1};
+  double least = 1e300;
+  for (int i = 0; i < 7; ++i) {
+    const Tile& t = TILES[i];
+    const int64_t tiles = ceil_div(out, t.wa) * ceil_div(n, t.wb), nk = ceil_div(in, 128);
+    for (int s = 1; s <= 8; s *= 2) {
+      if (s > 1 && (tiles * s > 512 || nk < 4 * s)) break;
+      const double rounds = tiles * s / 256.0;
+      double us = (i < 3 ? std::max(1.0, rounds) : std::ceil(rounds)) * (ceil_div(nk, s) * t.step + t.rest);
+      if (s > 1) us += 3.2 + (s + 1) * (double)n * out * 1e-6;
+      if (us < least) least = us, best = {i, s};
+    }
+  }
+  return best;
 }
 
 template <bool YBF16>
 void matmul_go(int tile, dim3 grid, hipStream_t stream, const MatmulArgs& g) {
-#define GPTQ_GO(W, B, OCC) hipLaunchKernelGGL((k_int8_matmul<YBF16, W, W, B, B, OCC>), grid, dim3(256), 0, stream, g)
-  if (tile == 2) GPTQ_GO(256, 4, 1);
-  else if (tile == 1) GPTQ_GO(128, 2, 2);
-  else GPTQ_GO(64, 1, 3);
+#define GPTQ_GO(I, OCC)                                                                                                    \
+  case I:                                                                                                                  \
+    hipLaunchKernelGGL((k_int8_matmul<YBF16, TILES[I].wa, TILES[I].wb, TILES[I].wa / 64, TILES[I].wb / 64, TILES[I].ring, OCC>), \
+                       grid, dim3(256), 0, stream, g);                                                                     \
+    break
+  switch (tile) {
+    GPTQ_GO(0, 2);
+    GPTQ_GO(1, 2);
+    GPTQ_GO(2, 2);
+    GPTQ_GO(3, 1);
+    GPTQ_GO(4, 1);
+    GPTQ_GO(5, 1);
+    GPTQ_GO(6, 1);
+  }
 #undef GPTQ_GO
 }
 
 }  // namespace
 
 size_t int8_matmul_ws_bytes(int64_t n, int64_t in, int64_t out) {
+  if (n <= INT8_FEW) return 0;
   const MatmulPlan p = matmul_plan(n, in, out);
   return p.slices > 1 ? align_up((size_t)p.slices * n * out * 4, 256) : 0;
 }
 
 hipError_t int8_matmul_launch(const Int8Matrix& a, const Int8Matrix& w, const float* bias, int relu, void* Y, int y_dtype,
                               int64_t ld_y, void* ws, hipStream_t stream) {
+  if (a.rows <= INT8_FEW) return int8_matmul_few_launch(a, w, bias, relu, Y, y_dtype, ld_y, stream);
   const MatmulPlan p = matmul_plan(a.rows, a.cols, w.rows);
+  const Tile& shape = TILES[p.tile];
   const bool bf16 = y_dtype == GPTQ_BF16;
   MatmulArgs g = {};
   g.kp = (int)int8_code_row(a.cols);
   g.wc = w.codes, g.ws = w.scales, g.bias = bias, g.out = (int)w.rows, g.relu = relu;
-  g.ta = (int)ceil_div(w.rows, 64 << p.tile), g.nk = (int)ceil_div(a.cols, 128);
+  g.ta = (int)ceil_div(w.rows, shape.wa), g.nk = (int)ceil_div(a.cols, 128);
   g.slice = (int)ceil_div(g.nk, p.slices);
   const int slices = (int)ceil_div(g.nk, g.slice);
-  // at most 2^20 tiles a launch
-  const int64_t rows_max = p.slices > 1 ? a.rows : std::max<int64_t>(1, ((int64_t)1 << 20) / g.ta) * (64 << p.tile);
+  // at most 2^20 tiles a launch (sums over slices have far fewer)
+  const int64_t rows_max = p.slices > 1 ? a.rows : std::max<int64_t>(1, ((int64_t)1 << 20) / g.ta) * shape.wb;
   for (int64_t r = 0; r < a.rows; r += rows_max) {
     g.n = std::min(rows_max, a.rows - r);
-    g.tb = (int)ceil_div(g.n, 64 << p.tile);
+    g.tb = (int)ceil_div(g.n, shape.wb);
     g.ac = a.codes + r * g.kp, g.as = a.scales + r;
     g.Y = static_cast<uint8_t*>(Y) + r * ld_y * (bf16 ? 2 : 4), g.ld = ld_y;
     if (slices > 1) g.Y = ws, g.ld = w.rows;
-    const dim3 grid(tile_grid((int64_t)g.ta * g.tb, p.tile == 2 ? 256 : 1 << 30), (unsigned)slices);
+    const dim3 grid(tile_grid((int64_t)g.ta * g.tb, shape.wa == 256 ? 256 : 1 << 30), (unsigned)slices);
     bf16 ? matmul_go<true>(p.tile, grid, stream, g) : matmul_go<false>(p.tile, grid, stream, g);
   }
   if (slices > 1) {
     g.Y = Y, g.ld = ld_y;
-    const dim3 grid((unsigned)std::min<int64_t>(2048, ceil_div(a.rows * w.rows, 256)));
-    hipLaunchKernelGGL(bf16 ? k_int8_join<true> : k_int8_join<false>, grid, dim3(256), 0, stream, g,
-                       static_cast<const int*>(ws), slices);
+    const bool four = w.rows % 4 == 0;
+    const dim3 grid((unsigned)std::min<int64_t>(8192, ceil_div(a.rows * (four ? w.rows / 4 : w.rows), 256)));
+    const auto kernel = four ? (bf16 ? k_int8_join<true, 4> : k_int8_join<false, 4>)
+                             : (bf16 ? k_int8_join<true, 1> : k_int8_join<false, 1>);
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, g, static_cast<const int*>(ws), slices);
   }
   return hipGetLastError();
 }
 
 size_t int8_linear_ws_bytes(int64_t n, int64_t in, int64_t out) {
+  if (int8_few_fused(n, in)) return 0;
   return align_up(n * int8_code_row(in), 256) + align_up(n * 4, 256) + int8_matmul_ws_bytes(n, in, out);
 }
 
 hipError_t int8_linear_launch(const void* X, int x_dtype, int64_t n, int64_t ld_x, const Int8Matrix& w, const float* bias,
                               int relu, void* Y, int y_dtype, int64_t ld_y, void* ws, hipStream_t stream) {
+  if (int8_few_fused(n, w.cols)) return int8_linear_few_launch(X, x_dtype, n, ld_x, w, bias, relu, Y, y_dtype, ld_y, stream);
   int8_t* codes = static_cast<int8_t*>(ws);
   float* scales = reinterpret_cast<float*>(codes + align_up(n * int8_code_row(w.cols), 256));
   uint8_t* rest = reinterpret_cast<uint8_t*>(scales) + align_up(n * 4, 256);

@@ -1,6 +1,6 @@
-// The tile product that the large kernels of the MX and the 8-bit integer operators share: a workgroup of four waves forms WA x WB of the sum over
-// k of a(i, k) b(j, k), operands streaming from memory straight into a ring of LDS stages while the matrix cores work
-// on earlier ones.
+// The tile product that the large kernels of the MX and the 8-bit integer operators share: a workgroup of four waves forms
+// WA x WB of the sum over k of a(i, k) b(j, k), operands streaming from memory straight into a ring of LDS stages while the
+// matrix cores work on earlier ones.
 //
 // What bounds it: LDS and the L2. A 32 x 32 product of two fragments reads both of them, 2 KB, for 32 cycles of the
 // matrix core (bf16 and 4-bit elements). A wave of 128 x 128 reads 8 fragments for 16 products, 16 B per matrix-core
@@ -9,13 +9,13 @@
 // for: a stage therefore takes whole lines, 128 bytes of each row (64 bytes of each row, twice, cost 2.5 times the
 // lines of the 4-bit product at 16384 x 4096 x 11008 with its scales, 16 TB/s, which was the limit).
 //
-// A stage holds four steps of k (64 columns each for MX, 16 for bf16, 32 for int8), two stages make the ring. The fragments of a step
-// are read between the products of the step before. Before the last step of a stage its buffer has been read by all
+// A stage holds four steps of k (64 columns each for MX, 16 for bf16, 32 for int8), two stages make the ring (more of
+// them for small int8 tiles). The fragments of a step are read between the products of the step before. Before the last step of a stage its buffer has been read by all
 // waves and the next stage has arrived (one wait, one barrier); between its products go the first fragments of the next
 // stage and the transfers of the stage after that, which have until the next such point to land.
 //
-// Stage layout. Operands whose k runs along a row (E2M1, E4M3, bf16, int8) keep 128 bytes of each row together (E4M3: two such
-// planes); the 16-byte chunks of row r are permuted by XOR with the Gray code of r, so that the consecutive rows that
+// Stage layout. Operands whose k runs along a row (E2M1, E4M3, bf16, int8) keep 128 bytes of each row together (E4M3: two
+// such planes); the 16-byte chunks of row r are permuted by XOR with the Gray code of r, so that the consecutive rows that
 // one ds_read_b128 takes at one logical chunk lie on different banks. Operands whose k runs down the columns (bf16, "T")
 // keep each k's row together and are read by the transposing ds_read_b64_tr_b16; chunks are permuted by bits of k.
 #pragma once
@@ -217,7 +217,8 @@ __device__ __forceinline__ i32x8 as_operand(const int (&f)[N]) {
 // A (first operand) x B (second): KA is K_E2M1 with KB K_E2M1 or K_E4M3, or both are bf16 kinds, or both K_INT8 (whose
 // sums are whole numbers in 32 bits, kept as the bits of acc).
 // E4M3 fragments are multiplied in two parts (see split_e4m3).
-template <int KA, int KB, int WA, int WB, int MB, int NB>
+// RING: stages in LDS. What arrives is one stage of them ahead of what is multiplied, the others are on their way.
+template <int KA, int KB, int WA, int WB, int MB, int NB, int RING = 2>
 struct TileProduct {
   static constexpr int NW = 4;
   static constexpr bool MX = KA == K_E2M1;
@@ -232,7 +233,7 @@ struct TileProduct {
   // ring fills with the next one's first stages; the small ones', of which several share a CU, through the ring's.
   static constexpr bool STAYS = MB == 4;
   static constexpr int PB = STAYS && !MX ? 2 : 1;
-  static constexpr int LDS = 2 * STAGE + SCALES + (STAYS ? NW * 4096 * PB : 0);
+  static constexpr int LDS = RING * STAGE + SCALES + (STAYS ? NW * 4096 * PB : 0);
   static constexpr int SI = MX ? ((WA + WB) / 32 + NW - 1) / NW : 0;  // scale transfers per wave (some twice)
   static constexpr int PER = A::NI + B::NI;
   static constexpr int NM = MB * NB;
@@ -240,18 +241,15 @@ struct TileProduct {
   // and second. All of them between the last step's products saturate the L1's 64 bytes a cycle while the matrix cores
   // wait (16384 x 4096 x 11008 in 4 bits: 478 us, against 444); spread over all four steps the last ones arrive late (455).
   static constexpr int D3 = PER * 8 / 16, D0 = PER * 12 / 16, D1 = PER;
-  // Large int8 tiles hold the fragments of all four steps: those of the next stage's first three are read during the last
-  // step and those of its fourth during its own first, so that a buffer is free for the stage after next from a stage's second
-  // step on. Transfers then have up to six steps to land instead of four; shares as above, in the second, third and fourth
-  // step. us for 16384 x 4096 x 11008 with the shares of two steps' fragments 717, with these 672 (4, 8, 12 of 16: 665, 8, 16,
-  // 16: 667; all in the second step: 681).
-  static constexpr bool DEEP = KA == K_INT8 && MB == 4;
+  // int8 in a ring of two holds the fragments of all four steps: those of the next stage's first three are read during the
+  // last step and those of its fourth during its own first, so that a buffer is free for the stage after next from a stage's
+  // second step on. Transfers then have up to six steps to land instead of four; shares as above, of the second, third and
+  // fourth step. us for 16384 x 4096 x 11008 with two steps' fragments 717, with these 672 (shares 4, 8, 12 of 16 with the
+  // rest in the next stage's first step 665, all in the second step 681). Small tiles with longer rings do without
+  // (200 x 4096 x 4096 in a ring of four 11.0, with four steps' fragments and their second barrier 11.6).
+  static constexpr bool DEEP = KA == K_INT8 && RING == 2;
   static constexpr int SETS = DEEP ? 4 : 2;
-#ifndef I8C1
-#define I8C1 6
-#define I8C2 11
-#endif
-  static constexpr int C1 = PER * I8C1 / 16, C2 = PER * I8C2 / 16;
+  static constexpr int C1 = PER * 6 / 16, C2 = PER * 11 / 16;
   static_assert(!MX || (WA % 64 == 0 && WB % 64 == 0), "scale transfers");
 
   A a;
@@ -281,7 +279,7 @@ struct TileProduct {
       const int row = 32 * stile[i] + (lane >> 1);
       svoff[i] = (uint32_t)((row < WA ? row : row - WA) * srow + ((lane & 1) ^ swz2(row)) * 16);
     }
-    soff = (uint32_t)(2 * STAGE + (lane & 31) * 32 + swz2(lane) * 16);
+    soff = (uint32_t)(RING * STAGE + (lane & 31) * 32 + swz2(lane) * 16);
     clear();
   }
 
@@ -300,7 +298,7 @@ struct TileProduct {
 #pragma unroll
     for (int i = 0; i < SI; ++i) {
       dma16_unless(skip, 32 * stile[i] < WA ? ra : rb,
-                   (uint32_t)__builtin_amdgcn_readfirstlane((int)(base + 2 * STAGE + stile[i] * 1024)), svoff[i]);
+                   (uint32_t)__builtin_amdgcn_readfirstlane((int)(base + RING * STAGE + stile[i] * 1024)), svoff[i]);
     }
   }
 
@@ -404,15 +402,15 @@ struct TileProduct {
   // behind: transfers and stores (at least) that were issued since the next stage's transfers, or 0 if that is not known
   template <int BEHIND>
   __device__ __forceinline__ void deep_stage(int at, int nk, int behind) {
-    constexpr int F = MB + NB;
-    const uint32_t other = STAGE - slot;
+    constexpr int F = MB + NB, W = (RING - 2) * PER + C2;
+    const uint32_t other = RING == 2 ? STAGE - slot : slot == (RING - 1) * STAGE ? 0u : slot + STAGE;
     deep_step<0, 3 * F, 4 * F, 0, 0>(slot, slot);
     wait_and_barrier<63>();  // all waves have read all of the stage
-    const bool cross = at + 2 == nk;
+    const bool cross = at + RING == nk;
     a.mem.take_if(cross, an), b.mem.take_if(cross, bn);
     deep_step<1, 0, 0, 0, C1>(slot, slot);
     deep_step<2, 0, 0, C1, C2>(slot, slot);
-    wait_and_barrier_or<C2, (C2 + BEHIND < 63 ? C2 + BEHIND : 63)>(behind);
+    wait_and_barrier_or<W, (W + BEHIND < 63 ? W + BEHIND : 63)>(behind);
     deep_step<3, 0, 3 * F, C2, PER>(other, slot);
     slot = other;
   }
@@ -420,13 +418,14 @@ struct TileProduct {
   // stage `at` of nk, the P-th of a pair
   template <int P>
   __device__ __forceinline__ void stage(int at, int nk) {
-    const uint32_t other = STAGE - slot;
+    const uint32_t other = RING == 2 ? STAGE - slot : slot == (RING - 1) * STAGE ? 0u : slot + STAGE;
+    const uint32_t last = RING == 2 ? other : slot == 0 ? (RING - 1) * STAGE : slot - STAGE;
     if constexpr (MX) take_scales<P>();
-    step<0, D3, D0>(slot, other);
-    step<1, D0, D1>(slot, other);
-    step<2, D1, D1>(slot, other);
-    wait_and_barrier<0>();
-    const bool cross = at + 2 == nk;  // the next stage to bring is the next tile's first
+    step<0, D3, D0>(slot, last);
+    step<1, D0, D1>(slot, last);
+    step<2, D1, D1>(slot, last);
+    wait_and_barrier<(RING - 2) * PER>();
+    const bool cross = at + RING == nk;  // the next stage to bring is the next tile's first
     a.mem.take_if(cross, an), b.mem.take_if(cross, bn);
     if constexpr (MX) {
       // Scale bytes are read two stages at a time. Those of the four stages that the buffer holds have all been read
@@ -449,12 +448,14 @@ struct TileProduct {
   // scale bytes behind a row's last block at 0).
   __device__ __forceinline__ void start() {
     if constexpr (MX) transfer_scales(0, sa, sb);
-#pragma unroll
-    for (int i = 0; i < PER; ++i) transfer(i, 0);
     constexpr int AHEAD = DEEP ? PER : D3;
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i) transfer(i, STAGE);
-    wait_and_barrier<AHEAD>();
+    for (int s = 0; s < RING - 1; ++s)
+#pragma unroll
+      for (int i = 0; i < PER; ++i) transfer(i, s * STAGE);
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) transfer(i, (RING - 1) * STAGE);
+    wait_and_barrier<(RING - 2) * PER + AHEAD>();
     static_for<0, (DEEP ? 3 : 1) * (MB + NB)>([&](auto t) {
       constexpr int S = decltype(t)::value / (MB + NB);
       read_frag<S, S, decltype(t)::value % (MB + NB)>(0);
