@@ -54,6 +54,7 @@ struct NormArgs {
 };
 hipError_t rms_norm_launch(const NormArgs& a, int x_dtype, int r_dtype, int fmt, hipStream_t stream);
 
+// norm_grad.hip
 struct NormGradArgs {
   const void *dy, *h, *dh;
   int64_t ldy, ldh, lddh, n;
@@ -63,7 +64,7 @@ struct NormGradArgs {
   int64_t lddx;
   int accumulate;
   float* dweight;
-  double* part;  // rows of d partial sums of dweight
+  double* part;  // rows of d partial sums of dweight, one for each workgroup
 };
 size_t rms_norm_grad_ws_bytes(int64_t n, int64_t d);
 hipError_t rms_norm_grad_launch(const NormGradArgs& a, int y_dtype, int h_dtype, hipStream_t stream);

@@ -34,38 +34,6 @@ __device__ __forceinline__ i32x4 load16(__amdgpu_buffer_rsrc_t r, int off) {
   return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
 }
 
-// Columns c .. c + 7 of a row of `in` >= 8, zeros behind the last: the row's last eight are loaded instead of what lies past its
-// end, and moved down.
-template <bool XBF16>
-__device__ __forceinline__ Chunk<XBF16> load_shifted(const void* __restrict__ X, int64_t row, int c, int in) {
-  constexpr int W = XBF16 ? 4 : 8;
-  const int from = min(c, in - 8), s = c - from;
-  const i32x4_any* p = reinterpret_cast<const i32x4_any*>(static_cast<const uint8_t*>(X) + (row + from) * (XBF16 ? 2 : 4));
-  Chunk<XBF16> r;
-#pragma unroll
-  for (int q = 0; q < W / 4; ++q) {
-    const i32x4 v = p[q];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) r.w[4 * q + e] = (uint32_t)v[e];
-  }
-  if (s > 0) {
-#pragma unroll
-    for (int b = W / 2; b > 0; b /= 2) {
-      const bool on = s >= 8 || (s & (XBF16 ? 2 * b : b));
-#pragma unroll
-      for (int q = 0; q < W; ++q) {
-        const uint32_t next = q + b < W ? r.w[q + b < W ? q + b : 0] : 0u;
-        r.w[q] = s >= 8 ? 0u : on ? next : r.w[q];
-      }
-    }
-    if (XBF16 && (s & 1)) {
-#pragma unroll
-      for (int q = 0; q < W; ++q) r.w[q] = r.w[q] >> 16 | (q + 1 < W ? r.w[q + 1 < W ? q + 1 : 0] << 16 : 0u);
-    }
-  }
-  return r;
-}
-
 // The n tokens on their way to codes and scales in LDS, rows of `stride` bytes. n up to 8: 8 waves, or 4, 2, 1, share a token;
 // more: a wave takes two. A lane holds at most eight times 8 columns (int8_few_fused) from the token's maximum to its codes.
 template <bool XBF16>
@@ -86,16 +54,21 @@ struct FewTokens {
     times = (a.kp + 512 * per - 1) / (512 * per);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (used(a, i)) x[i] = load_shifted<XBF16>(a.X, token(i) * a.ldx, column(i), a.in);
+      if (used(a, i)) x[i] = load_full<XBF16>(a.X, token(i) * a.ldx + min(column(i), a.in - 8));
   }
   __device__ __forceinline__ void quantize(const FewArgs& a, int8_t* codes, int stride, float* scales, uint32_t* tops) {
     uint32_t top[2] = {0, 0};
 #pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int over = column(i) - (a.in - 8);  // past the row's end: its last eight columns were read
+      if (used(a, i) && over > 0) move_down<XBF16>(x[i], over);
+    }
+#pragma unroll
     for (int i = 0; i < 8; ++i)
       if (used(a, i)) top[i >> 2] = max(top[i >> 2], max_bits<XBF16>(chunk_max<XBF16>(x[i])));
     if (!two) top[0] = max(top[0], top[1]);
-    top[0] = wave_max(top[0]);
-    if (two) top[1] = wave_max(top[1]);
+    top[0] = lanes_max<64>(top[0]);
+    if (two) top[1] = lanes_max<64>(top[1]);
     if (per > 1) {
       if ((threadIdx.x & 63) == 0) tops[wave] = top[0];
       __syncthreads();

@@ -11,23 +11,28 @@ namespace gptq {
 
 namespace {
 
-template <bool XBF16, int NCH>
+template <bool XBF16, int NCH, int LANES>
 __global__ __launch_bounds__(1024) void k_int8_quantize(const void* __restrict__ X, int64_t ld, int64_t n, int d, int kp,
                                                         RowShape rs, int8_t* __restrict__ codes,
                                                         float* __restrict__ scales) {
   __shared__ RowShared shared;
-  RowGroup g;
+  RowGroup<LANES> g;
   g.init(rs);
+  if (LANES < 64 && g.slot >= rs.rows) return;
+  Tail tail;
+  tail.init(g.column(NCH - 1), d);
   for (int64_t r0 = (int64_t)blockIdx.x * rs.rows; r0 < n; r0 += (int64_t)gridDim.x * rs.rows) {
     const int64_t row = r0 + g.slot;
     Chunk<XBF16> x[NCH];
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-      const int c = g.column(i);
-      x[i] = load_chunk<XBF16>(X, row * ld + c, c, row < n ? d : 0);
-      top = max(top, max_bits<XBF16>(chunk_max<XBF16>(x[i])));
+      const int64_t at = min(row, n - 1) * ld;
+      x[i] = i < NCH - 1 ? load_full<XBF16>(X, at + g.column(i)) : tail.load<XBF16>(X, at, d);
     }
+    tail.settle(x[NCH - 1], d);
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) top = max(top, max_bits<XBF16>(chunk_max<XBF16>(x[i])));
     top = g.max_of_row(top, shared);
     const float s = int8_scale(top);
     const bool finite = top < 0x7F800000u;
@@ -41,7 +46,7 @@ __global__ __launch_bounds__(1024) void k_int8_quantize(const void* __restrict__
         for (int q = 0; q < 8; ++q) v[q] = chunk_at<XBF16>(x[i], q);
         if (c < kp) *reinterpret_cast<uint2*>(codes + row * kp + c) = finite ? int8_encode(v, s, inv) : make_uint2(0u, 0u);
       }
-      if (g.lane_of_row == 0) scales[row] = s;
+      if (g.lane == 0) scales[row] = s;
     }
   }
 }
@@ -86,14 +91,13 @@ constexpr int64_t MAX_UNITS = (int64_t)1 << 25;
 hipError_t int8_quantize_launch(const void* X, int x_dtype, int64_t n, int64_t in, int64_t ld_x, int8_t* codes,
                                 float* scales, hipStream_t stream) {
   const int kp = (int)int8_code_row(in);
-  const RowShape rs = row_shape(ceil_div(in, 512), n);
-  const dim3 grid(row_grid(rs, n)), block(rs.threads());
-#define GPTQ_GO(N)                                                                                                       \
-  if (x_dtype == GPTQ_BF16)                                                                                              \
-    hipLaunchKernelGGL((k_int8_quantize<true, N>), grid, block, 0, stream, X, ld_x, n, (int)in, kp, rs, codes, scales);  \
-  else                                                                                                                   \
-    hipLaunchKernelGGL((k_int8_quantize<false, N>), grid, block, 0, stream, X, ld_x, n, (int)in, kp, rs, codes, scales)
-  GPTQ_ROW_CHUNKS(rs.chunks, GPTQ_GO)
+  const RowShape rs = row_shape(in, n, 4);
+  const dim3 grid((unsigned)std::min<int64_t>(ceil_div(n, rs.rows), (int64_t)4 * 256 * (2048 / rs.threads()))), block(rs.threads());
+  const bool b = x_dtype == GPTQ_BF16;
+#define GPTQ_GO(N, L)                                                                                                   \
+  hipLaunchKernelGGL((b ? k_int8_quantize<true, N, L> : k_int8_quantize<false, N, L>), grid, block, 0, stream, X, ld_x, n, \
+                     (int)in, kp, rs, codes, scales)
+  GPTQ_ROW_SHAPE(rs, GPTQ_GO)
 #undef GPTQ_GO
   return hipGetLastError();
 }
