@@ -17,14 +17,34 @@ from dataclasses import dataclass
 
 import torch
 
+from ._lib import GPTQ_BF16, GPTQ_F32
 from .gptq import QuantResult, _dtype_code, _on, _req_cuda
 from .mx import _bias_ptr, _call, _empty, _matrix, _need, _out_code, _result, _stream, _workspace
 
 __all__ = ["Int8Tensor", "int8_quantize", "int8_dequantize", "int8_weight", "int8_matmul", "int8_linear"]
 
 
+_TYPES = {torch.float32: GPTQ_F32, torch.bfloat16: GPTQ_BF16}
+
+
 def _code_row(cols: int) -> int:
-    return -(-cols // 128) * 128
+    return (cols + 127) & -128
+
+
+def _rows(t: torch.Tensor, name: str) -> int:
+    """Checks a row-major device matrix; its leading dimension. (The ordinary case in one pass: a call's kernels may take
+    only a few microseconds.)"""
+    s = t.shape
+    if len(s) == 2 and t.is_cuda:
+        ld, one = t.stride()
+        if one == 1 and ld >= s[1] > 0:
+            return ld
+    return _matrix(t, name)
+
+
+def _type(t: torch.Tensor) -> int:
+    code = _TYPES.get(t.dtype)
+    return _dtype_code(t) if code is None else code
 
 
 @dataclass
@@ -55,10 +75,10 @@ def _int8(t: Int8Tensor, name: str, device: int | None = None, cols: int | None 
     if not isinstance(t, Int8Tensor):
         raise TypeError(f"{name} must be an Int8Tensor")
     c, s, d = t.codes, t.scales, t.cols
-    n = c.shape[0]
-    if (c.is_cuda and s.is_cuda and d >= 1 and (cols is None or d == cols) and c.dtype == torch.int8
-            and s.dtype == torch.float32 and c.shape == (n, _code_row(d)) and s.shape == (n,) and c.is_contiguous()
-            and s.is_contiguous() and c.get_device() == s.get_device() and (device is None or c.get_device() == device)):
+    n, dev = c.shape[0], c.get_device()
+    if (dev >= 0 and (device is None or dev == device) and (cols is None or d == cols) and d >= 1
+            and c.dtype is torch.int8 and s.dtype is torch.float32 and c.shape == (n, _code_row(d)) and s.shape == (n,)
+            and c.is_contiguous() and s.is_contiguous() and s.get_device() == dev):
         return
     if not (c.is_cuda and s.is_cuda):
         raise ValueError(f"{name} must hold device tensors")
@@ -95,24 +115,30 @@ def _share_memory(a: torch.Tensor, b: torch.Tensor) -> bool:
 
 
 def _apart(out, name: str, *operands) -> None:
-    """Refuses a result, if one was given, that shares memory with an operand."""
-    if out is None or out.numel() == 0 or out.dim() > 2:
+    """Refuses a given result that shares memory with an operand."""
+    if out.numel() == 0 or out.dim() > 2:
         return
+    a, _, step, rows = _extent(out)
+    b = a + step * rows
     for t in operands:
-        if t is not None and t.numel() and _share_memory(out, t):
+        if t is None or t.numel() == 0:
+            continue
+        p = t.data_ptr()
+        if p >= b or (t.is_contiguous() and p + t.nbytes <= a):
+            continue
+        if _share_memory(out, t):
             raise ValueError(f"{name} shares memory with an operand")
 
 
 def int8_quantize(X: torch.Tensor, stream=None) -> Int8Tensor:
     """X (n x cols, bf16 or fp32; 3-D inputs are flattened to tokens) -> Int8Tensor, a scale for each row and codes
     -127 .. 127 rounded to nearest-even. A row that is not finite becomes NaN."""
-    _req_cuda(X, "X")
     if X.dim() == 3:
+        _req_cuda(X, "X")
         with _on(stream):  # tokens that no view flattens are copied there, and the copy belongs to it
             X = X.reshape(-1, X.shape[-1])
-    ld = _matrix(X, "X")
+    ld, xt = _rows(X, "X"), _type(X)
     n, d = X.shape
-    xt = _dtype_code(X)
     codes = _empty((n, _code_row(d)), torch.int8, X, stream)
     scales = _empty((n,), torch.float32, X, stream)
     dev = X.get_device()
@@ -125,7 +151,8 @@ def int8_dequantize(Q: Int8Tensor, dtype=torch.bfloat16, out: torch.Tensor | Non
     _int8(Q, "Q")
     yt = _out_code(dtype)
     c, n, d = Q.codes, Q.codes.shape[0], Q.cols
-    _apart(out, "out", c, Q.scales)
+    if out is not None:
+        _apart(out, "out", c, Q.scales)
     Y, ld = _result(out, "out", (n, d), dtype, c, stream)
     dev = c.get_device()
     _call("gptq_int8_dequantize", dev, c.data_ptr(), Q.scales.data_ptr(), n, d, Y.data_ptr(), yt, ld, _stream(stream, dev))
@@ -165,7 +192,8 @@ def int8_matmul(A: Int8Tensor, W: Int8Tensor, bias: torch.Tensor | None = None, 
     yt = _out_code(dtype)
     no = W.codes.shape[0]
     b = _bias_ptr(bias, no, c)
-    _apart(out, "out", c, A.scales, W.codes, W.scales, bias)
+    if out is not None:
+        _apart(out, "out", c, A.scales, W.codes, W.scales, bias)
     Y, ld = _result(out, "out", (n, no), dtype, c, stream)
     need = _need("gptq_int8_matmul_workspace_bytes", n, d, no)
     ws, wp = _workspace(need, c, stream)
@@ -178,15 +206,19 @@ def int8_linear(X: torch.Tensor, W: Int8Tensor, bias: torch.Tensor | None = None
                 out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Y = Q(X) W^T (+ bias, then ReLU): X (n x in, bf16 or fp32) is quantized on its way into the product, the results
     being those of int8_quantize and int8_matmul. dtype None: X's."""
-    ldx = _matrix(X, "X")
+    ldx, xt = _rows(X, "X"), _type(X)
     n, d = X.shape
     dev = X.get_device()
     _int8(W, "W", dev, d)
-    dtype = X.dtype if dtype is None else dtype
-    xt, yt = _dtype_code(X), _out_code(dtype)
+    yt = xt
+    if dtype is None:
+        dtype = X.dtype
+    else:
+        yt = _out_code(dtype)
     no = W.codes.shape[0]
     b = _bias_ptr(bias, no, X)
-    _apart(out, "out", X, W.codes, W.scales, bias)
+    if out is not None:
+        _apart(out, "out", X, W.codes, W.scales, bias)
     Y, ld = _result(out, "out", (n, no), dtype, X, stream)
     need = _need("gptq_int8_linear_workspace_bytes", n, d, no)
     ws, wp = _workspace(need, X, stream)

@@ -23,10 +23,9 @@ from typing import NamedTuple
 import torch
 
 from ._lib import GPTQ_NORM_E4M3, GPTQ_NORM_INT8
-from .gptq import _dtype_code
-from .int8 import Int8Tensor, _apart
+from .int8 import Int8Tensor, _apart, _rows, _type
 from .int8 import _code_row as _int8_code_row
-from .mx import MXTensor, _call, _empty, _matrix, _need, _result, _scale_row, _stream, _workspace
+from .mx import MXTensor, _call, _empty, _need, _result, _scale_row, _stream, _workspace
 from .mx import _code_row as _mx_code_row
 
 __all__ = ["NormResult", "rms_norm", "rms_norm_grad"]
@@ -40,11 +39,18 @@ class NormResult(NamedTuple):
     rstd: torch.Tensor        # float32 [n]
 
 
-def _operand(t: torch.Tensor, name: str, shape, like: torch.Tensor, dtype=None) -> int:
-    ld = _matrix(t, name)
-    if t.shape != shape or t.device != like.device or (dtype is not None and t.dtype != dtype):
-        raise ValueError(f"{name} must be a {dtype or 'bfloat16 or float32'} tensor of shape {tuple(shape)} on {like.device}")
+def _operand(t: torch.Tensor, name: str, like: torch.Tensor, dtype=None) -> int:
+    ld = _rows(t, name)
+    if t.shape != like.shape or t.get_device() != like.get_device() or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{name} must be a {dtype or 'bfloat16 or float32'} tensor of shape {tuple(like.shape)} on "
+                         f"{like.device}")
     return ld
+
+
+def _vector(t: torch.Tensor, name: str, size: int, device: int) -> int:
+    if t.get_device() != device or t.dtype is not torch.float32 or t.shape != (size,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor of shape {(size,)} on device {device}")
+    return t.data_ptr()
 
 
 def rms_norm(X: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: torch.Tensor | None = None,
@@ -56,23 +62,21 @@ def rms_norm(X: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual:
         code = _FMT[fmt]
     except (KeyError, TypeError):
         raise ValueError(f"unknown format {fmt!r} ('int8' or 'e4m3')") from None
-    ldx = _matrix(X, "X")
+    ldx, xt = _rows(X, "X"), _type(X)
     n, d = X.shape
     dev = X.get_device()
-    xt = _dtype_code(X)
-    w = _vector(weight, "weight", d, X)
+    w = _vector(weight, "weight", d, dev)
     rp = hp = None
     rt = ldr = ldh = 0
     h = X
     if residual is not None:
-        ldr = _operand(residual, "residual", X.shape, X)
-        rt = _dtype_code(residual)
-        _apart(out, "out", X, weight)
-        same = out is not None and out.data_ptr() == residual.data_ptr() and out.stride() == residual.stride()
-        if not same:
-            _apart(out, "out", residual)
+        ldr, rt = _operand(residual, "residual", X), _type(residual)
+        rp = residual.data_ptr()
+        if out is not None:
+            same = out is residual or (out.data_ptr() == rp and out.stride() == residual.stride())
+            _apart(out, "out", X, weight, None if same else residual)
         h, ldh = _result(out, "out", (n, d), residual.dtype, X, stream)
-        rp, hp = residual.data_ptr(), h.data_ptr()
+        hp = h.data_ptr()
     elif out is not None:
         raise ValueError("out is given without a residual: h is X")
     if code == GPTQ_NORM_INT8:
@@ -89,39 +93,32 @@ def rms_norm(X: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual:
     return NormResult(y, h, rstd)
 
 
-def _vector(t: torch.Tensor, name: str, size: int, like: torch.Tensor) -> int:
-    if t.device != like.device or t.dtype != torch.float32 or t.shape != (size,) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous float32 tensor of shape {(size,)} on {like.device}")
-    return t.data_ptr()
-
-
 def rms_norm_grad(dY: torch.Tensor, H: torch.Tensor, rstd: torch.Tensor, weight: torch.Tensor,
                   dH: torch.Tensor | None = None, out: torch.Tensor | None = None, weight_out: torch.Tensor | None = None,
                   accumulate: bool = False, stream=None):
     """The gradients of X (and alike of the residual), in H's type, and of the weight, fp32, from dY, the gradient of
     rms_norm's y, and its h and rstd. dH: the gradient of h itself, added to X's. accumulate adds the weight's gradient to
     weight_out. Returns (dX, dweight)."""
-    ldy = _matrix(dY, "dY")
+    ldy, yt = _rows(dY, "dY"), _type(dY)
     n, d = dY.shape
     dev = dY.get_device()
-    yt = _dtype_code(dY)
-    ldh = _operand(H, "H", dY.shape, dY)
-    ht = _dtype_code(H)
-    r, w = _vector(rstd, "rstd", n, dY), _vector(weight, "weight", d, dY)
+    ldh, ht = _operand(H, "H", dY), _type(H)
+    r, w = _vector(rstd, "rstd", n, dev), _vector(weight, "weight", d, dev)
     sp, lds = None, 0
     if dH is not None:
-        lds = _operand(dH, "dH", dY.shape, dY, H.dtype)
+        lds = _operand(dH, "dH", dY, H.dtype)
         sp = dH.data_ptr()
     if accumulate and weight_out is None:
         raise ValueError("accumulate adds to weight_out: pass it")
-    _apart(out, "out", dY, H, rstd, weight, dH, weight_out)
+    if out is not None:
+        _apart(out, "out", dY, H, rstd, weight, dH, weight_out)
     dX, ldx = _result(out, "out", (n, d), H.dtype, dY, stream)
     if weight_out is None:
         dw = _empty((d,), torch.float32, dY, stream)
         dwp = dw.data_ptr()
     else:
         _apart(weight_out, "weight_out", dY, H, rstd, weight, dH)
-        dw, dwp = weight_out, _vector(weight_out, "weight_out", d, dY)
+        dw, dwp = weight_out, _vector(weight_out, "weight_out", d, dev)
     need = _need("gptq_rms_norm_grad_workspace_bytes", n, d)
     ws, wp = _workspace(need, dY, stream)
     _call("gptq_rms_norm_grad", dev, dY.data_ptr(), yt, ldy, H.data_ptr(), ht, ldh, r, w, sp, lds, n, d,
