@@ -29,10 +29,16 @@ size_t int8_linear_ws_bytes(int64_t n, int64_t in, int64_t out);
 hipError_t int8_linear_launch(const void* X, int x_dtype, int64_t n, int64_t ld_x, const Int8Matrix& w, const float* bias,
                               int relu, void* Y, int y_dtype, int64_t ld_y, void* ws, hipStream_t stream);
 
-// int8_few.hip: the same for at most INT8_FEW tokens, in codes or, where they are small enough, quantized on their way in
-constexpr int INT8_FEW = 16;
+// int8_few.hip: the same for few tokens, in codes or, where they are small enough, quantized on their way in. us against the tile
+// product: 17 x 4096 x 4096 6.7 / 9.5, 32 x 4096 x 4096 8.0 / 9.7, 32 x 512 x 512 2.9 / 4.6, but 24 x 11008 x 4096 18 / 17 and
+// 24 x 4096 x 11008 (two rounds of workgroups, each loading all tokens) 19 / 15.
+static inline bool int8_few(int64_t n, int64_t in, int64_t out) {
+  return n <= 16 || (n <= 32 && in <= 4096 && out <= 4096);
+}
+// us of GPU time so / with a launch to quantize them, which also costs a call 3 us on the host: 1 x 4096 x 4096 7.3 / 8.3,
+// 8 x 4096 x 4096 10.5 / 8.9, 16 x 4096 x 4096 (too many) - / 9.4.
 static inline bool int8_few_fused(int64_t n, int64_t in) {
-  return n <= INT8_FEW && in >= 8 && (n <= 2 ? n : n <= 4 ? 4 : n <= 8 ? 8 : 16) * in <= 8 * 4096;
+  return n <= 16 && in >= 8 && (n <= 2 ? n : n <= 4 ? 4 : n <= 8 ? 8 : 16) * in <= 8 * 4096;
 }
 hipError_t int8_matmul_few_launch(const Int8Matrix& x, const Int8Matrix& w, const float* bias, int relu, void* Y, int y_dtype,
                                   int64_t ld_y, hipStream_t stream);

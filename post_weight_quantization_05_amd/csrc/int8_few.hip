@@ -1,4 +1,4 @@
-// Y = A W^T s_a s_w (+ bias) (ReLU) for at most 16 tokens, in codes or quantized on their way in: the form for single tokens.
+// Y = A W^T s_a s_w (+ bias) (ReLU) for few tokens (int8_few), in codes or quantized on their way in: the form for single tokens.
 //
 // What bounds it is the latency of a launch and the reading of W (16.8 MB for 4096 x 4096, 3.4 us at the rate of a large copy).
 // A workgroup forms 16 rows of W on its own, its eight waves splitting the sum over k and joining their parts in LDS.
@@ -92,10 +92,11 @@ struct FewTokens {
   }
 };
 
-template <int SRC, bool YBF16>
+// NT: groups of 16 tokens. UC: 64s of columns that are loaded together.
+template <int SRC, bool YBF16, int NT, int UC>
 __global__ __launch_bounds__(64 * FEW_WAVES) void k_int8_few(const FewArgs a) {
   extern __shared__ __attribute__((aligned(16))) int8_t codes[];  // FROM_CODES: none
-  __shared__ int red[FEW_WAVES][16][20];
+  __shared__ int red[FEW_WAVES][16 * NT][20];
   __shared__ float scales[16];
   __shared__ uint32_t tops[FEW_WAVES];
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
@@ -109,27 +110,35 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void k_int8_few(const FewArgs a) {
   const int off = r * a.kp + 16 * g;
   const int8_t* lds = codes + min(r, a.n - 1) * stride + 16 * g;  // tokens past the last repeat it and are not used
   struct Part {
-    i32x4 w[8], x[8];
+    i32x4 w[UC], x[NT][UC];
   };
-  // 512 columns from unit u; what lies past the last 64 repeats them and is not used
+  // columns from the u-th UC 64s on; what lies past the last 64 repeats them and is not used
   auto load = [&](Part& p, int u) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int c = min(8 * u + j, chunks - 1) * 64;
+    for (int j = 0; j < UC; ++j) {
+      const int c = min(UC * u + j, chunks - 1) * 64;
       p.w[j] = load16(w, off + c);
-      if (SRC == FROM_CODES) p.x[j] = load16(x, off + c);
+      if (SRC == FROM_CODES) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) p.x[t][j] = load16(x, off + c + t * 16 * a.kp);
+      }
     }
   };
-  i32x4 acc = {0, 0, 0, 0};
+  i32x4 acc[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) acc[t] = (i32x4){0, 0, 0, 0};
   auto multiply = [&](Part& p, int u) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (8 * u + j >= chunks) break;
-      const i32x4 t = SRC == FROM_CODES ? p.x[j] : *reinterpret_cast<const i32x4*>(lds + (8 * u + j) * 64);
-      acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(p.w[j], t, acc, 0, 0, 0);
+    for (int j = 0; j < UC; ++j) {
+      if (UC * u + j >= chunks) break;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const i32x4 v = SRC == FROM_CODES ? p.x[t][j] : *reinterpret_cast<const i32x4*>(lds + (UC * u + j) * 64);
+        acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(p.w[j], v, acc[t], 0, 0, 0);
+      }
     }
   };
-  const int units = (chunks + 7) / 8;
+  const int units = (chunks + UC - 1) / UC;
   Part even, odd;
   if constexpr (SRC != FROM_CODES) {
     // loads come back in their order: the tokens first, whose codes are made while W is on its way
@@ -152,12 +161,13 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void k_int8_few(const FewArgs a) {
     __builtin_amdgcn_sched_barrier(0);
     if (v < units) multiply(odd, v);
   }
-  // register i of lane 16 g + r: W's row 4 g + i, token r
-  *reinterpret_cast<i32x4*>(&red[wave][r][4 * g]) = acc;
+  // register i of lane 16 g + r: W's row 4 g + i, token r of its group
+#pragma unroll
+  for (int t = 0; t < NT; ++t) *reinterpret_cast<i32x4*>(&red[wave][16 * t + r][4 * g]) = acc[t];
   __syncthreads();
-  if (threadIdx.x < 256) {
-    const int tok = threadIdx.x / 16, o = threadIdx.x % 16, c = o0 + o;
-    if (tok >= a.n || c >= a.out) return;
+  for (int e = threadIdx.x; e < 256 * NT; e += 64 * FEW_WAVES) {
+    const int tok = e / 16, o = e % 16, c = o0 + o;
+    if (tok >= a.n || c >= a.out) continue;
     int sum = 0;
 #pragma unroll
     for (int i = 0; i < FEW_WAVES; ++i) sum += red[i][tok][o];
@@ -168,11 +178,11 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void k_int8_few(const FewArgs a) {
   }
 }
 
-template <int SRC>
+template <int SRC, int NT, int UC>
 hipError_t few_go(const FewArgs& a, int y_dtype, hipStream_t stream) {
   const size_t lds = SRC == FROM_CODES ? 0 : (size_t)a.n * (a.kp + 16);
-  hipLaunchKernelGGL((y_dtype == GPTQ_BF16 ? k_int8_few<SRC, true> : k_int8_few<SRC, false>), dim3((unsigned)ceil_div(a.out, 16)),
-                     dim3(64 * FEW_WAVES), lds, stream, a);
+  hipLaunchKernelGGL((y_dtype == GPTQ_BF16 ? k_int8_few<SRC, true, NT, UC> : k_int8_few<SRC, false, NT, UC>),
+                     dim3((unsigned)ceil_div(a.out, 16)), dim3(64 * FEW_WAVES), lds, stream, a);
   return hipGetLastError();
 }
 
@@ -182,14 +192,15 @@ hipError_t int8_matmul_few_launch(const Int8Matrix& x, const Int8Matrix& w, cons
                                   int64_t ld_y, hipStream_t stream) {
   const FewArgs a = {x.codes, x.scales, 0, w.codes, w.scales, bias, Y, ld_y, (int)x.rows, (int)w.cols,
                      (int)int8_code_row(w.cols), (int)w.rows, relu};
-  return few_go<FROM_CODES>(a, y_dtype, stream);
+  if (x.rows <= 16) return few_go<FROM_CODES, 1, 8>(a, y_dtype, stream);
+  return few_go<FROM_CODES, 2, 4>(a, y_dtype, stream);
 }
 
 hipError_t int8_linear_few_launch(const void* X, int x_dtype, int64_t n, int64_t ld_x, const Int8Matrix& w, const float* bias,
                                   int relu, void* Y, int y_dtype, int64_t ld_y, hipStream_t stream) {
   const FewArgs a = {X, nullptr, ld_x, w.codes, w.scales, bias, Y, ld_y, (int)n, (int)w.cols,
                      (int)int8_code_row(w.cols), (int)w.rows, relu};
-  return x_dtype == GPTQ_BF16 ? few_go<FROM_BF16>(a, y_dtype, stream) : few_go<FROM_F32>(a, y_dtype, stream);
+  return x_dtype == GPTQ_BF16 ? few_go<FROM_BF16, 1, 8>(a, y_dtype, stream) : few_go<FROM_F32, 1, 8>(a, y_dtype, stream);
 }
 
 }  // namespace gptq

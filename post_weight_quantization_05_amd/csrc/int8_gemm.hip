@@ -292,14 +292,14 @@ void matmul_go(int tile, dim3 grid, hipStream_t stream, const MatmulArgs& g) {
 }  // namespace
 
 size_t int8_matmul_ws_bytes(int64_t n, int64_t in, int64_t out) {
-  if (n <= INT8_FEW) return 0;
+  if (int8_few(n, in, out)) return 0;
   const MatmulPlan p = matmul_plan(n, in, out);
   return p.slices > 1 ? align_up((size_t)p.slices * n * out * 4, 256) : 0;
 }
 
 hipError_t int8_matmul_launch(const Int8Matrix& a, const Int8Matrix& w, const float* bias, int relu, void* Y, int y_dtype,
                               int64_t ld_y, void* ws, hipStream_t stream) {
-  if (a.rows <= INT8_FEW) return int8_matmul_few_launch(a, w, bias, relu, Y, y_dtype, ld_y, stream);
+  if (int8_few(a.rows, a.cols, w.rows)) return int8_matmul_few_launch(a, w, bias, relu, Y, y_dtype, ld_y, stream);
   const MatmulPlan p = matmul_plan(a.rows, a.cols, w.rows);
   const Tile& shape = TILES[p.tile];
   const bool bf16 = y_dtype == GPTQ_BF16;
