@@ -1,9 +1,9 @@
 // Y = A W^T s_a s_w (+ bias) (ReLU) for few tokens (int8_few), in codes or quantized on their way in: the form for single tokens.
 //
 // What bounds it is the latency of a launch and the reading of W (16.8 MB for 4096 x 4096, 3.4 us at the rate of a large copy).
-// A workgroup forms 16 rows of W on its own, its eight waves splitting the sum over k and joining their parts in LDS.
+// A workgroup forms 16 rows of W on its own, its waves splitting the sum over k and joining their parts in LDS.
 // v_mfma_i32_16x16x64_i8 multiplies: lane l = 16 g + r of an operand holds row r, columns 16 g .. 16 g + 15 of the 64. A wave
-// has the loads of 512 columns in flight before the first product of the 512 before them.
+// has its next loads in flight before the first product of those before.
 //
 // Few tokens are quantized by every workgroup, which saves a launch: its waves share them out, find each token's largest
 // magnitude and leave the codes in LDS, while W's first columns are on their way.
@@ -16,7 +16,6 @@ namespace gptq {
 
 namespace {
 
-constexpr int FEW_WAVES = 8;
 enum { FROM_CODES = 0, FROM_F32 = 1, FROM_BF16 = 2 };
 
 struct FewArgs {
@@ -92,13 +91,15 @@ struct FewTokens {
   }
 };
 
-// NT: groups of 16 tokens. UC: 64s of columns that are loaded together.
-template <int SRC, bool YBF16, int NT, int UC>
-__global__ __launch_bounds__(64 * FEW_WAVES) void k_int8_few(const FewArgs a) {
+// NT: groups of 16 tokens. NW: waves. UC: 64s of columns that are loaded together. 16 waves and 128 columns for codes: 1 x 4096 x
+// 11008 10.9 us, 12 x 11008 x 4096 14.2 (8 waves and 512 columns 12.9 and 15.2, 256 columns 11.5 and 14.3, 64 columns and 16
+// waves 12.4 and 16.1; loads of W past the caches' reuse change nothing).
+template <int SRC, bool YBF16, int NT, int NW, int UC>
+__global__ __launch_bounds__(64 * NW) void k_int8_few(const FewArgs a) {
   extern __shared__ __attribute__((aligned(16))) int8_t codes[];  // FROM_CODES: none
-  __shared__ int red[FEW_WAVES][16 * NT][20];
+  __shared__ int red[NW][16 * NT][20];
   __shared__ float scales[16];
-  __shared__ uint32_t tops[FEW_WAVES];
+  __shared__ uint32_t tops[8];
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int o0 = blockIdx.x * 16;
@@ -152,12 +153,12 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void k_int8_few(const FewArgs a) {
   } else if (wave < units) {
     load(even, wave);
   }
-  for (int u = wave; u < units; u += 2 * FEW_WAVES) {
-    const int v = u + FEW_WAVES;
+  for (int u = wave; u < units; u += 2 * NW) {
+    const int v = u + NW;
     if (v < units) load(odd, v);
     __builtin_amdgcn_sched_barrier(0);
     multiply(even, u);
-    if (v + FEW_WAVES < units) load(even, v + FEW_WAVES);
+    if (v + NW < units) load(even, v + NW);
     __builtin_amdgcn_sched_barrier(0);
     if (v < units) multiply(odd, v);
   }
@@ -165,12 +166,12 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void k_int8_few(const FewArgs a) {
 #pragma unroll
   for (int t = 0; t < NT; ++t) *reinterpret_cast<i32x4*>(&red[wave][16 * t + r][4 * g]) = acc[t];
   __syncthreads();
-  for (int e = threadIdx.x; e < 256 * NT; e += 64 * FEW_WAVES) {
+  for (int e = threadIdx.x; e < 256 * NT; e += 64 * NW) {
     const int tok = e / 16, o = e % 16, c = o0 + o;
     if (tok >= a.n || c >= a.out) continue;
     int sum = 0;
 #pragma unroll
-    for (int i = 0; i < FEW_WAVES; ++i) sum += red[i][tok][o];
+    for (int i = 0; i < NW; ++i) sum += red[i][tok][o];
     const float y = int8_result((float)sum, SRC == FROM_CODES ? a.xs[tok] : scales[tok], a.ws[c], a.bias ? a.bias[c] : 0.f,
                                 a.relu ? 0.f : -__builtin_inff());
     if (YBF16) static_cast<uint16_t*>(a.Y)[tok * a.ldy + c] = (uint16_t)bf16_bits(y);
@@ -178,11 +179,11 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void k_int8_few(const FewArgs a) {
   }
 }
 
-template <int SRC, int NT, int UC>
+template <int SRC, int NT, int NW, int UC>
 hipError_t few_go(const FewArgs& a, int y_dtype, hipStream_t stream) {
   const size_t lds = SRC == FROM_CODES ? 0 : (size_t)a.n * (a.kp + 16);
-  hipLaunchKernelGGL((y_dtype == GPTQ_BF16 ? k_int8_few<SRC, true, NT, UC> : k_int8_few<SRC, false, NT, UC>),
-                     dim3((unsigned)ceil_div(a.out, 16)), dim3(64 * FEW_WAVES), lds, stream, a);
+  hipLaunchKernelGGL((y_dtype == GPTQ_BF16 ? k_int8_few<SRC, true, NT, NW, UC> : k_int8_few<SRC, false, NT, NW, UC>),
+                     dim3((unsigned)ceil_div(a.out, 16)), dim3(64 * NW), lds, stream, a);
   return hipGetLastError();
 }
 
@@ -192,15 +193,15 @@ hipError_t int8_matmul_few_launch(const Int8Matrix& x, const Int8Matrix& w, cons
                                   int64_t ld_y, hipStream_t stream) {
   const FewArgs a = {x.codes, x.scales, 0, w.codes, w.scales, bias, Y, ld_y, (int)x.rows, (int)w.cols,
                      (int)int8_code_row(w.cols), (int)w.rows, relu};
-  if (x.rows <= 16) return few_go<FROM_CODES, 1, 8>(a, y_dtype, stream);
-  return few_go<FROM_CODES, 2, 4>(a, y_dtype, stream);
+  if (x.rows <= 16) return few_go<FROM_CODES, 1, 16, 2>(a, y_dtype, stream);
+  return few_go<FROM_CODES, 2, 8, 4>(a, y_dtype, stream);
 }
 
 hipError_t int8_linear_few_launch(const void* X, int x_dtype, int64_t n, int64_t ld_x, const Int8Matrix& w, const float* bias,
                                   int relu, void* Y, int y_dtype, int64_t ld_y, hipStream_t stream) {
   const FewArgs a = {X, nullptr, ld_x, w.codes, w.scales, bias, Y, ld_y, (int)n, (int)w.cols,
                      (int)int8_code_row(w.cols), (int)w.rows, relu};
-  return x_dtype == GPTQ_BF16 ? few_go<FROM_BF16, 1, 8>(a, y_dtype, stream) : few_go<FROM_F32, 1, 8>(a, y_dtype, stream);
+  return x_dtype == GPTQ_BF16 ? few_go<FROM_BF16, 1, 8, 8>(a, y_dtype, stream) : few_go<FROM_F32, 1, 8, 8>(a, y_dtype, stream);
 }
 
 }  // namespace gptq

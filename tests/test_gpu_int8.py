@@ -65,7 +65,8 @@ def _check(y, product, bias=None, relu=False):
 
 # ---- quantization -------------------------------------------------------------------------------------------
 QSIZES = [(1, 1), (1, 8), (3, 31), (5, 127), (4, 128), (3, 129), (7, 512), (2, 513), (6, 1025), (1, 4096), (33, 1000),
-          (300, 352), (5, 4104), (1, 11008), (3, 16385), (2, 40000), (2, 65536)]
+          (300, 352), (5, 4104), (1, 11008), (3, 16385), (2, 40000), (2, 65536), (2003, 100), (1501, 200), (700, 64), (3001, 5),
+          (5000, 513), (3000, 2100)]
 
 
 def _same_quantization(q, x64):

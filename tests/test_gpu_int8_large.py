@@ -1,0 +1,115 @@
+"""The integer product at sizes that take its large tiles, workgroups that pass from one tile to the next, and far offsets.
+
+Sums are whole numbers and every kernel finishes them by the same two fp32 multiplications, so without a bias the result is
+known to the last bit: fp32(sum) times the token's scale, times the channel's, each rounded once. Runs are repeated, since a
+missing wait would show now and then.
+"""
+import pytest
+import torch
+
+import post_weight_quantization_05_amd as G
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("no GPU", allow_module_level=True)
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def _operand(g, rows, d):
+    kp = -(-d // 128) * 128
+    c = torch.zeros((rows, kp), dtype=torch.int8, device="cuda")
+    c[:, :d] = torch.randint(-127, 128, (rows, d), generator=g, device="cuda", dtype=torch.int16).to(torch.int8)
+    return G.Int8Tensor(c, torch.rand(rows, generator=g, device="cuda") + 0.5, d)
+
+
+def _sums(a, w):
+    """Exact: partial sums over 1024 columns stay below 2^24, their total below 2^53."""
+    total = torch.zeros((a.rows, w.rows), dtype=torch.float64, device="cuda")
+    for k in range(0, a.codes.shape[1], 1024):
+        total += a.codes[:, k:k + 1024].float() @ w.codes[:, k:k + 1024].float().t()
+    return total
+
+
+def _expected(total, a, w):
+    return (total.float() * a.scales[:, None]) * w.scales
+
+
+# 256 x 256, 256 x 192 and 256 x 128 tiles by the fitted times, several rounds of them, whole and cut off at every side, with
+# even and odd numbers of 128 columns
+SIZES = [(8000, 4096, 8000), (8192, 1100, 8192), (2048, 4096, 11008), (2001, 3900, 10999), (2048, 11008, 4096),
+         (1999, 5000, 4099), (4096, 4096, 4096), (12000, 2050, 6001), (1646, 2688, 3554), (540, 5635, 9735),
+         (7872, 8832, 1468), (2240, 4864, 1777), (8832, 2286, 279), (448, 9729, 790), (2743, 1580, 3836)]
+
+
+@pytest.mark.parametrize("y", ["f32", "bf16"])
+@pytest.mark.parametrize("n,d,out", SIZES)
+def test_matmul_bit_for_bit(n, d, out, y):
+    print(f"[int8 matmul large] {n}x{d}x{out} -> {y}", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(n + out)
+    a, w = _operand(g, n, d), _operand(g, out, d)
+    total = _sums(a, w)
+    want = _expected(total, a, w).to(DT[y])
+    for _ in range(4):
+        assert torch.equal(G.int8_matmul(a, w, dtype=DT[y]), want)
+    bias = torch.randn(out, generator=g, device="cuda") * 1e4
+    got = G.int8_matmul(a, w, bias=bias, relu=True, dtype=torch.float32)
+    # the last multiplication and the addition are one step: half a step of the result, and of the sum times its scale
+    product = (total.float() * a.scales[:, None]).double() * w.scales.double()
+    ref = torch.relu(product + bias.double())
+    assert float(((got.double() - ref).abs() - 1.001 * 2.0 ** -24 * ref).max()) <= 0
+
+
+def test_matmul_while_other_streams_store():
+    """The same product on two streams at once, each with its own result and workspace."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    a, w = _operand(g, 3000, 2100), _operand(g, 5000, 2100)
+    want = _expected(_sums(a, w), a, w).bfloat16()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [G.int8_matmul(a, w, dtype=torch.bfloat16, stream=s) for _ in range(4) for s in streams]
+    torch.cuda.synchronize()
+    assert all(torch.equal(t, want) for t in got)
+
+
+@pytest.mark.parametrize("y", ["f32", "bf16"])
+@pytest.mark.parametrize("n,d,out", [(5, 300, 500), (300, 700, 600), (520, 2048, 4100)])
+def test_matmul_far_rows(n, d, out, y):
+    """Rows of the result further apart than 2^24 bytes, the last ones beyond 2^32."""
+    ld = (1 << 23) + 5
+    g = torch.Generator(device="cuda").manual_seed(n)
+    a, w = _operand(g, n, d), _operand(g, out, d)
+    far = torch.empty(((n - 1) * ld + out + 3,), dtype=DT[y], device="cuda").as_strided((n, out + 3), (ld, 1))
+    far.fill_(7.0)
+    G.int8_matmul(a, w, dtype=DT[y], out=far[:, 1:1 + out])
+    assert torch.equal(far[:, 1:1 + out], _expected(_sums(a, w), a, w).to(DT[y]))
+    assert (far[:, 0] == 7).all() and (far[:, 1 + out:] == 7).all()
+
+
+def test_captured_twice_with_replays_between():
+    """Two graphs of products over slices and of the layer, replayed in turn and among eager calls."""
+    g = torch.Generator(device="cuda").manual_seed(7)
+    sizes = [(64, 11008, 512), (300, 6300, 200)]
+    ops = [(_operand(g, n, d), _operand(g, out, d), torch.randn((n, d), generator=g, device="cuda").bfloat16())
+           for n, d, out in sizes]
+
+    def step(i):
+        a, w, x = ops[i]
+        return G.int8_matmul(a, w), G.int8_linear(x, w)
+
+    want = [[t.clone() for t in step(i)] for i in range(2)]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for i in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(step(i))
+        graphs.append(graph)
+    for _ in range(3):
+        for i in (0, 1, 1, 0):
+            graphs[i].replay()
+            eager = step(1 - i)
+            torch.cuda.synchronize()
+            assert all(torch.equal(p, q) for p, q in zip(outs[i], want[i]))
+            assert all(torch.equal(p, q) for p, q in zip(eager, want[1 - i]))

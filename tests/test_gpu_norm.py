@@ -64,7 +64,7 @@ def _check_norm(res, h64, w64, fmt, eps=EPS):
 
 
 SIZES = [(1, 1), (1, 8), (3, 31), (5, 127), (4, 128), (3, 129), (7, 512), (2, 513), (6, 1025), (1, 4096), (33, 1000),
-         (300, 352), (5, 4104), (1, 11008), (3, 16385), (2, 40000), (2, 65536)]
+         (300, 352), (5, 4104), (1, 11008), (3, 16385), (2, 40000), (2, 65536), (2003, 100), (1501, 200), (701, 5)]
 
 
 @pytest.mark.parametrize("fmt", ["int8", "e4m3"])
@@ -194,7 +194,7 @@ def _check_grad(dx, dw, dy, h, rstd, w, dh=None, base=None):
 @pytest.mark.parametrize("dh", [False, True])
 @pytest.mark.parametrize("y", ["f32", "bf16"])
 @pytest.mark.parametrize("hx", ["f32", "bf16"])
-@pytest.mark.parametrize("n,d", SIZES + [(2100, 256), (1500, 1000)])
+@pytest.mark.parametrize("n,d", SIZES + [(2100, 256), (1500, 1000), (9000, 40), (1300, 2500), (700, 11000)])
 def test_norm_grad(n, d, hx, y, dh):
     print(f"[rms_norm_grad] {n}x{d} h {hx} dy {y} dH {dh}", flush=True)
     rng = np.random.default_rng(n + 3 * d)
