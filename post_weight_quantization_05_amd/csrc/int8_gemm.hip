@@ -24,6 +24,7 @@ struct MatmulArgs {
   int out, ta, tb;   // tiles along out and along tokens
   int nk, slice;     // 128s of columns; those of a slice
   int relu;
+  int past;          // results leave past the caches' reuse
 };
 
 // What a wave needs of the scales and the bias for its results, 32 MB columns by 32 NB rows: they come by transfers to LDS
@@ -67,9 +68,8 @@ struct WaveScales {
 };
 
 // Writes a wave's results: register i of lane l of acc[mb][nb] is row 32 nb + l % 32, column 32 mb + 8 (i / 4) + 4 (l / 32) + i % 4.
-// The sums go through LDS, 32 PB columns of 32 rows at a time, so that a store takes runs of 128 bytes of a row or more; they
-// leave past the caches' reuse (nontemporal: 643 against 659 us at 16384 x 4096 x 11008). Returns the stores that
-// a wave inside Y has issued, 0 at an edge. RAW: the sums themselves, to partial results.
+// The sums go through LDS, 32 PB columns of 32 rows at a time, so that a store takes runs of 128 bytes of a row or more. Returns
+// whether the wave's results lie inside Y, each store then being issued. RAW: the sums themselves, to partial results.
 template <bool YBF16, bool RAW, int PB, int MB, int NB>
 __device__ __forceinline__ int store_int8(const f32x16 (&acc)[MB][NB], uint8_t* lds, const WaveScales<MB, NB>& sc,
                                           const MatmulArgs& g, void* __restrict__ Y, int64_t ld, int64_t row0, int c0) {
@@ -129,8 +129,9 @@ __device__ __forceinline__ int store_int8(const f32x16 (&acc)[MB][NB], uint8_t* 
             o = __builtin_bit_cast(i32x4, (f32x4){v[0], v[1], v[2], v[3]});
           // No scalar offset: behind a 16-byte store with one the compiler leaves out the wait state before a vector
           // instruction that writes its data registers, and here such stores took the new contents now and then.
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o), to,
-                                                 first + ((nb * 32 + it * STEP) * step + 32 * m0 * ES), 0, 2);
+          const int at = first + ((nb * 32 + it * STEP) * step + 32 * m0 * ES);
+          if (g.past) __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o), to, at, 0, 2);
+          else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o), to, at, 0, 0);
         } else {
           const int64_t row = row0 + nb * 32 + lane / PER_ROW + it * STEP;
           const int c = c0 + 32 * m0 + (lane % PER_ROW) * V, n = row < g.n ? g.out - c : 0;
@@ -236,14 +237,14 @@ __global__ __launch_bounds__(256) void k_int8_join(const MatmulArgs g, const int
 }
 
 // Tiles (along out, along tokens), stages of the ring, and what a round of 256 of them takes, one to a CU: us for 128 columns
-// of k and for the rest. Fitted to 70 sizes from 17 x 102 x 64 to 16384 x 1344 x 11008: times off by 7 to 12 %, and the tile chosen by
-// them 1.4 % slower than the best one on average. The large tiles' rest is mostly that of all results leaving at once.
+// of k and for the rest. Fitted to 110 sizes from 17 x 65 x 64 to 16384 x 4096 x 11008; the tile that these times choose is 3 %
+// slower than the best one on average, 35 % at worst. The large tiles' rest is mostly that of all results leaving at once.
 struct Tile {
   int wa, wb, ring;
   double step, rest;
 };
-constexpr Tile TILES[] = {{64, 64, 4, 0.22, 1.4},   {128, 64, 3, 0.33, 2.0},   {128, 128, 2, 0.50, 3.7}, {128, 128, 4, 0.42, 4.4},
-                          {256, 128, 2, 0.67, 8.2}, {256, 192, 2, 0.86, 12.3}, {256, 256, 2, 1.02, 15.9}};
+constexpr Tile TILES[] = {{64, 64, 4, 0.23, 1.2},   {128, 64, 3, 0.38, 1.6},   {128, 128, 2, 0.56, 3.0}, {128, 128, 4, 0.47, 4.4},
+                          {256, 128, 2, 0.75, 7.6}, {256, 192, 2, 0.90, 12.2}, {256, 256, 2, 1.08, 15.8}};
 
 struct MatmulPlan {
   int tile;    // of TILES
@@ -316,6 +317,11 @@ hipError_t int8_matmul_launch(const Int8Matrix& a, const Int8Matrix& w, const fl
     g.tb = (int)ceil_div(g.n, shape.wb);
     g.ac = a.codes + r * g.kp, g.as = a.scales + r;
     g.Y = static_cast<uint8_t*>(Y) + r * ld_y * (bf16 ? 2 : 4), g.ld = ld_y;
+    // Whole lines leave past the caches' reuse (16384 x 4096 x 11008 630 us, with it 636; 8000 x 256 x 8000 49 and 55). Where
+    // rows are not aligned to lines, the caches have to join what two stores of the large tiles leave of one (11286 x 914 x
+    // 4830 with 256 x 256 tiles 114 us, past them 134).
+    const int line = p.tile < 4 ? 4 : 128;
+    g.past = slices == 1 && (reinterpret_cast<uintptr_t>(g.Y) | (uintptr_t)(ld_y * (bf16 ? 2 : 4))) % line == 0;
     if (slices > 1) g.Y = ws, g.ld = w.rows;
     const dim3 grid(tile_grid((int64_t)g.ta * g.tb, shape.wa == 256 ? 256 : 1 << 30), (unsigned)slices);
     bf16 ? matmul_go<true>(p.tile, grid, stream, g) : matmul_go<false>(p.tile, grid, stream, g);
