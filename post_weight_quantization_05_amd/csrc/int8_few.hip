@@ -1,4 +1,5 @@
-// Y = A W^T s_a s_w (+ bias) (ReLU) for few tokens (int8_few), in codes or quantized on their way in: the form for single tokens.
+// Y = A W^T s_a s_w (+ bias) (ReLU) for few tokens (int8_few), in codes or quantized on their way in: the form for single
+// tokens.
 //
 // What bounds it is the latency of a launch and the reading of W (16.8 MB for 4096 x 4096, 3.4 us at the rate of a large copy).
 // A workgroup forms 16 rows of W on its own, its waves splitting the sum over k and joining their parts in LDS.

@@ -9,10 +9,10 @@
 // for: a stage therefore takes whole lines, 128 bytes of each row (64 bytes of each row, twice, cost 2.5 times the
 // lines of the 4-bit product at 16384 x 4096 x 11008 with its scales, 16 TB/s, which was the limit).
 //
-// A stage holds four steps of k (64 columns each for MX, 16 for bf16, 32 for int8), two stages make the ring (more of
-// them for small int8 tiles). The fragments of a step are read between the products of the step before. Before the last step of a stage its buffer has been read by all
-// waves and the next stage has arrived (one wait, one barrier); between its products go the first fragments of the next
-// stage and the transfers of the stage after that, which have until the next such point to land.
+// A stage holds four steps of k (64 columns each for MX, 16 for bf16, 32 for int8), two stages make the ring (more of them for
+// small int8 tiles). The fragments of a step are read between the products of the step before. Before the last step of a stage
+// its buffer has been read by all waves and the next stage has arrived (one wait, one barrier); between its products go the
+// first fragments of the next stage and the transfers of the stage after that, which have until the next such point to land.
 //
 // Stage layout. Operands whose k runs along a row (E2M1, E4M3, bf16, int8) keep 128 bytes of each row together (E4M3: two
 // such planes); the 16-byte chunks of row r are permuted by XOR with the Gray code of r, so that the consecutive rows that

@@ -93,23 +93,30 @@ __global__ __launch_bounds__(NCH == 2 || NCH == 3 ? 512 : 1024) void k_rms_norm_
     }
     if (HOLD) rstd = a.rstd[min(row + step, a.n - 1)];
   }
-  // the workgroup's rows added in their order
+  // the workgroup's rows added in their order; the only workgroup's sums are the result
   extern __shared__ double sums[];
-  double* part = a.part + (int64_t)blockIdx.x * a.d;
-  double* to = rs.rows > 1 ? sums + (int64_t)g.slot * a.d : part;
+  const bool only = gridDim.x == 1;
+  auto leave = [&](int c, double v) {
+    if (only) a.dweight[c] = (float)(a.accumulate ? (double)a.dweight[c] + v : v);
+    else a.part[(int64_t)blockIdx.x * a.d + c] = v;
+  };
   if (g.slot < rs.rows) {
 #pragma unroll
     for (int i = 0; i < NCH; ++i)
 #pragma unroll
-      for (int q = 0; q < 8; ++q)
-        if (g.column(i) + q < a.d) to[g.column(i) + q] = dw[i][q];
+      for (int q = 0; q < 8; ++q) {
+        const int c = g.column(i) + q;
+        if (c >= a.d) continue;
+        if (rs.rows > 1) sums[g.slot * a.d + c] = dw[i][q];
+        else leave(c, dw[i][q]);
+      }
   }
   if (rs.rows == 1) return;
   __syncthreads();
   for (int c = threadIdx.x; c < a.d; c += blockDim.x) {
     double v = sums[c];
     for (int s = 1; s < rs.rows; ++s) v += sums[s * a.d + c];
-    part[c] = v;
+    leave(c, v);
   }
 }
 
@@ -132,14 +139,26 @@ __global__ __launch_bounds__(1024) void k_rms_norm_grad_join(const double* __res
 }
 
 // Workgroups of eight waves, of sixteen for rows of up to 2048 columns, and one of them to a CU: every one leaves a row of fp64
-// sums (16384 x 4096 with dh: 105 us so, 126 with two to a CU; 16384 x 256: 14.3 and 18).
-RowShape grad_shape(int64_t d, int64_t n) { return row_shape(d, n, d <= 2048 ? 16 : 8); }
-unsigned grad_grid(const RowShape& s, int64_t n) { return (unsigned)std::min<int64_t>(ceil_div(n, s.rows), 256); }
+// sums (16384 x 4096 with dh: 105 us so, 126 with two to a CU; 16384 x 256: 14.3 and 18). Up to 32768 values in up to four turns
+// go to a single one, which saves a call the second launch, 3.3 us on the host (64 x 512: 7.5 us of GPU time, 8 x 4096 10.5;
+// 512 x 64 would take eight turns, 14.5).
+struct GradPlan {
+  RowShape shape;
+  unsigned grid;
+};
+GradPlan grad_plan(int64_t d, int64_t n) {
+  const int waves = d <= 2048 ? 16 : 8;
+  const RowShape most = row_shape(d, 1 << 20, waves);
+  if (n * d <= 32768 && n <= 4 * most.rows) return {most, 1};
+  const RowShape s = row_shape(d, n, waves);
+  return {s, (unsigned)std::min<int64_t>(ceil_div(n, s.rows), 256)};
+}
 
 template <bool YBF16, bool HBF16, bool DH>
 void grad_go(const NormGradArgs& a, hipStream_t stream) {
-  const RowShape rs = grad_shape(a.d, a.n);
-  const dim3 grid(grad_grid(rs, a.n)), block(rs.threads());
+  const GradPlan p = grad_plan(a.d, a.n);
+  const RowShape rs = p.shape;
+  const dim3 grid(p.grid), block(rs.threads());
   const size_t lds = rs.rows > 1 ? rs.rows * a.d * sizeof(double) : 0;
 #define GPTQ_GO(N, L) hipLaunchKernelGGL((k_rms_norm_grad<YBF16, HBF16, DH, N, L>), grid, block, lds, stream, a, rs)
   GPTQ_ROW_SHAPE(rs, GPTQ_GO)
@@ -150,13 +169,14 @@ void grad_go(const NormGradArgs& a, hipStream_t stream) {
 
 size_t rms_norm_grad_ws_bytes(int64_t n, int64_t d) {
   if (n == 0) return 0;
-  return align_up((size_t)grad_grid(grad_shape(d, n), n) * d * 8, 256);
+  const unsigned grid = grad_plan(d, n).grid;
+  return grid > 1 ? align_up((size_t)grid * d * 8, 256) : 0;
 }
 
 hipError_t rms_norm_grad_launch(const NormGradArgs& a, int y_dtype, int h_dtype, hipStream_t stream) {
   int parts = 0;
   if (a.n > 0) {
-    parts = (int)grad_grid(grad_shape(a.d, a.n), a.n);
+    parts = (int)grad_plan(a.d, a.n).grid;
     const int kind = (y_dtype == GPTQ_BF16 ? 4 : 0) + (h_dtype == GPTQ_BF16 ? 2 : 0) + (a.dh ? 1 : 0);
     switch (kind) {
       case 0: grad_go<false, false, false>(a, stream); break;
@@ -169,7 +189,7 @@ hipError_t rms_norm_grad_launch(const NormGradArgs& a, int y_dtype, int h_dtype,
       default: grad_go<true, true, true>(a, stream); break;
     }
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    if (e != hipSuccess || parts == 1) return e;
   }
   hipLaunchKernelGGL(k_rms_norm_grad_join, dim3((unsigned)ceil_div(a.d, 32)), dim3(1024), 0, stream, a.part, parts, a.d,
                      a.accumulate, a.dweight);

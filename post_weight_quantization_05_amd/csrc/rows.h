@@ -13,10 +13,11 @@ struct RowShape {
   unsigned threads() const { return lanes < 64 ? (unsigned)ceil_div(rows * lanes, 64) * 64 : (unsigned)(64 * waves * rows); }
 };
 
-// For rows of d columns (at most 65536). Only a lane's last chunk may reach past the row's end. Two chunks a lane from 2049 columns on (norm of 16384 x 4096 without a residual: 39 us,
-// with one 50), three from 8193 on (8192 x 11008: 65 us, with eight in fewer waves 78). Half and quarter waves for short rows,
-// since what is done once a row and wave is most of their work (norm of 16384 x 256: 9.4 us, with whole waves 15).
-// waves: those of a workgroup where rows are short enough for several; few rows are spread over the chip's CUs first.
+// For rows of d columns (at most 65536). Only a lane's last chunk may reach past the row's end. Two chunks a lane from 2049
+// columns on (norm of 16384 x 4096 without a residual: 39 us, with one 50), three from 8193 on (8192 x 11008: 65 us, with eight
+// in fewer waves 78). Half and quarter waves for short rows, since what is done once a row and wave is most of their work
+// (norm of 16384 x 256: 9.4 us, with whole waves 15). waves: those of a workgroup where rows are short enough for several; few
+// rows are spread over the chip's CUs first.
 static inline RowShape row_shape(int64_t d, int64_t n, int waves) {
   const int64_t segments = ceil_div(d, 512);
   const int chunks = segments <= 4 ? 1 : segments <= 16 ? 2 : segments <= 24 ? 3 : segments <= 64 ? 4 : 8;

@@ -194,7 +194,8 @@ def _check_grad(dx, dw, dy, h, rstd, w, dh=None, base=None):
 @pytest.mark.parametrize("dh", [False, True])
 @pytest.mark.parametrize("y", ["f32", "bf16"])
 @pytest.mark.parametrize("hx", ["f32", "bf16"])
-@pytest.mark.parametrize("n,d", SIZES + [(2100, 256), (1500, 1000), (9000, 40), (1300, 2500), (700, 11000)])
+@pytest.mark.parametrize("n,d", SIZES + [(2100, 256), (1500, 1000), (9000, 40), (1300, 2500), (700, 11000), (64, 512), (65, 512),
+                                         (256, 128), (257, 128), (8, 4096), (9, 4096)])
 def test_norm_grad(n, d, hx, y, dh):
     print(f"[rms_norm_grad] {n}x{d} h {hx} dy {y} dH {dh}", flush=True)
     rng = np.random.default_rng(n + 3 * d)

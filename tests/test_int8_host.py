@@ -159,10 +159,10 @@ def test_norm_refusals():
     e4m3 = list(good)
     e4m3[12], e4m3[14] = 1, P + 4  # MX scale bytes start at 16-byte aligned addresses
     assert lib.gptq_rms_norm(*e4m3) == INVALID
-    need = lib.gptq_rms_norm_grad_workspace_bytes(4, 64)
+    need = lib.gptq_rms_norm_grad_workspace_bytes(4000, 64)
     assert need > 0
     #       dY yt ldy h  ht ldh rstd w dH ldd n  d  acc dX ldx dw ws need stream
-    good = [P, 0, 64, P, 1, 64, P, P, P, 64, 4, 64, 0, P, 64, P, P, need, None]
+    good = [P, 0, 64, P, 1, 64, P, P, P, 64, 4000, 64, 0, P, 64, P, P, need, None]
     _refused(lib.gptq_rms_norm_grad, good, [
         (0, None, INVALID), (0, P + 2, INVALID), (1, 2, INVALID), (2, 63, INVALID), (3, None, INVALID), (3, P + 1, INVALID),
         (4, -1, INVALID), (5, 63, INVALID), (6, None, INVALID), (7, None, INVALID), (7, P + 2, INVALID), (8, P + 1, INVALID),
