@@ -40,7 +40,9 @@ def _expected(total, a, w):
 # even and odd numbers of 128 columns
 SIZES = [(8000, 4096, 8000), (8192, 1100, 8192), (2048, 4096, 11008), (2001, 3900, 10999), (2048, 11008, 4096),
          (1999, 5000, 4099), (4096, 4096, 4096), (12000, 2050, 6001), (1646, 2688, 3554), (540, 5635, 9735),
-         (7872, 8832, 1468), (2240, 4864, 1777), (8832, 2286, 279), (448, 9729, 790), (2743, 1580, 3836)]
+         (7872, 8832, 1468), (2240, 4864, 1777), (8832, 2286, 279), (448, 9729, 790), (2743, 1580, 3836),
+         # smaller tiles in longer rings, and sums over slices
+         (200, 4096, 4096), (512, 4096, 4096), (1024, 4096, 4096), (64, 11008, 4096), (300, 2000, 900), (40, 130, 70)]
 
 
 @pytest.mark.parametrize("y", ["f32", "bf16"])
@@ -59,6 +61,18 @@ def test_matmul_bit_for_bit(n, d, out, y):
     product = (total.float() * a.scales[:, None]).double() * w.scales.double()
     ref = torch.relu(product + bias.double())
     assert float(((got.double() - ref).abs() - 1.001 * 2.0 ** -24 * ref).max()) <= 0
+
+
+@pytest.mark.parametrize("n,d,out", [(4500, 1100, 5000), (2048, 4096, 11008), (60, 700, 300), (9, 700, 300)])
+def test_matmul_of_row_ranges(n, d, out):
+    """Runs of rows whose scales start at 4-byte aligned addresses, into a result that starts at an odd element."""
+    g = torch.Generator(device="cuda").manual_seed(n)
+    a, w = _operand(g, n + 3, d).rows_slice(1, n + 1), _operand(g, out + 5, d).rows_slice(3, out + 3)
+    want = _expected(_sums(a, w), a, w)
+    for y in DT.values():
+        wide = torch.full((n, out + 2), 7.0, dtype=y, device="cuda")
+        G.int8_matmul(a, w, dtype=y, out=wide[:, 1:1 + out])
+        assert torch.equal(wide[:, 1:1 + out], want.to(y)) and (wide[:, 0] == 7).all() and (wide[:, -1] == 7).all()
 
 
 def test_matmul_while_other_streams_store():
