@@ -72,10 +72,14 @@ def rms_norm(X: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual:
     if residual is not None:
         ldr, rt = _operand(residual, "residual", X), _type(residual)
         rp = residual.data_ptr()
-        if out is not None:
-            same = out is residual or (out.data_ptr() == rp and out.stride() == residual.stride())
+        same = False
+        if out is not None:  # a single row's stride says nothing: the same bytes are the same row
+            same = out is residual or (out.data_ptr() == rp and out.shape == residual.shape
+                                       and (n == 1 or out.stride() == residual.stride()))
             _apart(out, "out", X, weight, None if same else residual)
         h, ldh = _result(out, "out", (n, d), residual.dtype, X, stream)
+        if same:
+            ldh = ldr
         hp = h.data_ptr()
     elif out is not None:
         raise ValueError("out is given without a residual: h is X")

@@ -1,0 +1,61 @@
+"""The norm of a single token in place, in a column range of a wider buffer: the step of a decode loop whose stream lies among
+other state. Its results are those of the same row out of place, bit for bit, and the buffer around it stays as it was."""
+import pytest
+import torch
+
+import post_weight_quantization_05_amd as G
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("no GPU", allow_module_level=True)
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("x,r", [("bf16", "f32"), ("f32", "bf16"), ("bf16", "bf16")])
+@pytest.mark.parametrize("n,d", [(1, 333), (1, 4096), (1, 5), (2, 333)])
+def test_norm_in_place_in_a_column_range(n, d, x, r, fmt):
+    print(f"[rms_norm in place] {n}x{d} {x} + {r} -> {fmt}", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(n + d)
+    xw = torch.randn((n, d + 9), generator=g, device="cuda").to(DT[x])
+    wide = torch.randn((n + 2, d + 67), generator=g, device="cuda").to(DT[r])
+    w = torch.randn(d, generator=g, device="cuda")
+    X, before = xw[:, 3:3 + d], wide.clone()
+    want = G.rms_norm(X, w, residual=before[1:1 + n, 1:1 + d], fmt=fmt)
+    h = wide[1:1 + n, 1:1 + d]
+    got = G.rms_norm(X, w, residual=h, out=h, fmt=fmt)
+    assert got.h is h and torch.equal(h, want.h)
+    for p, q in ((got.y.codes, want.y.codes), (got.y.scales, want.y.scales), (got.rstd, want.rstd)):
+        assert torch.equal(p, q)
+    before[1:1 + n, 1:1 + d] = want.h
+    assert torch.equal(wide, before)
+    if n == 1:  # the same row as a tensor of another stride
+        again = wide[1, 1:1 + d].view(1, d)
+        want = G.rms_norm(X, w, residual=h.clone(), fmt=fmt)
+        got = G.rms_norm(X, w, residual=h, out=again, fmt=fmt)
+        assert torch.equal(wide[1:2, 1:1 + d], want.h) and torch.equal(got.y.codes, want.y.codes)
+
+
+def test_norm_of_single_tokens_in_place_replayed():
+    """A captured decode step on its range of the buffer: every replay adds x once more."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x, w = torch.randn((1, 512), generator=g, device="cuda"), torch.randn(512, generator=g, device="cuda")
+    wide = torch.randn((3, 700), generator=g, device="cuda")
+    h, before = wide[1:2, 40:552], wide.clone()
+    eager = before[1:2, 40:552].clone()
+    G.rms_norm(x, w, residual=h, out=h)
+    h.copy_(eager)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        res = G.rms_norm(x, w, residual=h, out=h)
+    for _ in range(3):
+        want = G.rms_norm(x, w, residual=eager)
+        eager = want.h
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(h, eager) and torch.equal(res.y.codes, want.y.codes) and torch.equal(res.y.scales, want.y.scales)
+    before[1:2, 40:552] = eager
+    assert torch.equal(wide, before)

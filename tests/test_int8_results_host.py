@@ -1,0 +1,54 @@
+"""Results that the caller gives to the 8-bit integer operators and the norm (no GPU needed: the library is stood in for)."""
+import types
+
+import pytest
+import torch
+
+from post_weight_quantization_05_amd import _lib, int8, mx, norm
+from tests.test_int8_streams_host import _t, recorder  # noqa: F401
+from tests.test_streams_host import _Library
+
+STREAM = types.SimpleNamespace(cuda_stream=1)
+
+
+@pytest.fixture
+def calls(monkeypatch, recorder):  # noqa: F811
+    """The library's calls as (name, arguments)."""
+    seen = []
+
+    class Library(_Library):
+        def __getattr__(self, f):
+            if f.endswith("_bytes"):
+                return lambda *a: 256
+            return lambda *a: seen.append((f, a)) or 0
+
+    monkeypatch.setattr(_lib, "load", lambda path=None: Library())
+    monkeypatch.setattr(mx, "_current_device", lambda: 1)
+    return seen
+
+
+@pytest.mark.parametrize("n", [1, 2, 5])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_norm_in_place_passes_one_leading_dimension(calls, n, fmt):
+    """A residual that is updated in place has one leading dimension, whatever range of a wider buffer it is: the library
+    takes its address twice only with the same rows."""
+    x, weight, wide = _t((n, 333)), _t((333,)), _t((8, 400))
+    h = wide[:n, 1:334]
+    for out in (h, wide[:n, 1:334]):  # the residual itself, and another tensor of the same memory
+        assert norm.rms_norm(x, weight, residual=h, out=out, fmt=fmt, stream=STREAM).h is out
+    assert len(calls) == 2
+    for name, a in calls:
+        assert name == "gptq_rms_norm" and a[3] == a[10] == h.data_ptr() and a[5] == a[11] and a[5] >= 333
+
+
+def test_norm_in_place_by_a_single_row_of_another_stride(calls):
+    """The stride of a single row says nothing: the same bytes are the same row."""
+    x, weight, wide = _t((1, 333)), _t((333,)), _t((8, 400))
+    h, out = wide[2:3, 1:334], wide[2, 1:334].view(1, 333)
+    assert h.stride() != out.stride() and h.data_ptr() == out.data_ptr()
+    norm.rms_norm(x, weight, residual=h, out=out, stream=STREAM)
+    norm.rms_norm(x, weight, residual=out, out=h, stream=STREAM)
+    assert all(a[3] == a[10] and a[5] == a[11] >= 333 for _, a in calls) and len(calls) == 2
+    two = _t((2, 333))
+    with pytest.raises(ValueError, match="operand"):  # two rows of them are not the same
+        norm.rms_norm(two, weight, residual=wide[2:4, 1:334], out=wide.view(-1)[801:801 + 666].view(2, 333), stream=STREAM)
