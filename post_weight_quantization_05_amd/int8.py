@@ -92,10 +92,10 @@ def _int8(t: Int8Tensor, name: str, device: int | None = None, cols: int | None 
 
 
 def _extent(t: torch.Tensor):
-    """Address of a matrix's (or vector's) first byte, bytes of a row, bytes from one row to the next, rows."""
+    """Address of a matrix's (or vector's, or number's) first byte, bytes of a row, bytes from one row to the next, rows."""
     size = t.element_size()
-    if t.dim() == 1:
-        return t.data_ptr(), t.shape[0] * size, t.shape[0] * size, 1
+    if t.dim() < 2:
+        return t.data_ptr(), t.numel() * size, t.numel() * size, 1
     return t.data_ptr(), t.shape[1] * size, max(t.stride(0), t.shape[1]) * size, t.shape[0]
 
 

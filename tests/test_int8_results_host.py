@@ -52,3 +52,35 @@ def test_norm_in_place_by_a_single_row_of_another_stride(calls):
     two = _t((2, 333))
     with pytest.raises(ValueError, match="operand"):  # two rows of them are not the same
         norm.rms_norm(two, weight, residual=wide[2:4, 1:334], out=wide.view(-1)[801:801 + 666].view(2, 333), stream=STREAM)
+
+
+def _results():
+    """Every call that takes a given result, by the result's name: a function of that tensor."""
+    a = int8.Int8Tensor(_t((40, 128), torch.int8), _t((40,)), 64)
+    w = int8.Int8Tensor(_t((8, 128), torch.int8), _t((8,)), 64)
+    x, h, weight, rstd = _t((40, 64)), _t((40, 64)), _t((64,)), _t((40,))
+    f32, s = torch.float32, STREAM
+    return {
+        "int8_dequantize": lambda t: int8.int8_dequantize(a, dtype=f32, out=t, stream=s),
+        "int8_matmul": lambda t: int8.int8_matmul(a, w, out=t, stream=s),
+        "int8_linear": lambda t: int8.int8_linear(x, w, out=t, stream=s),
+        "rms_norm": lambda t: norm.rms_norm(x, weight, residual=h, out=t, stream=s),
+        "rms_norm_grad dX": lambda t: norm.rms_norm_grad(x, h, rstd, weight, out=t, stream=s),
+        "rms_norm_grad dweight": lambda t: norm.rms_norm_grad(x, h, rstd, weight, weight_out=t, stream=s),
+    }
+
+
+@pytest.mark.parametrize("shape", [(), (0,), (1,), (40,), (1, 1), (41, 64), (2, 40, 64), (1, 1, 1, 1)])
+@pytest.mark.parametrize("name", list(_results()))
+def test_results_of_another_shape_are_refused(calls, name, shape):
+    with pytest.raises(ValueError, match="must be a .*tensor of shape"):
+        _results()[name](_t(shape))
+    assert not calls
+
+
+def test_gradient_refuses_a_number_for_the_weights_gradient_beside_a_given_result(calls):
+    dx = _t((40, 64))
+    for number in (dx[3, 5], _t(())):  # within dX's memory and apart from it
+        with pytest.raises(ValueError):
+            norm.rms_norm_grad(_t((40, 64)), _t((40, 64)), _t((40,)), _t((64,)), out=dx, weight_out=number, stream=STREAM)
+    assert not calls
