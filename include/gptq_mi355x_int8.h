@@ -45,8 +45,10 @@ int gptq_int8_dequantize(const int8_t* codes, const float* scales, int64_t n, in
 int gptq_int8_pad_codes(const int8_t* codes, int64_t out, int64_t in, int8_t* padded, void* stream);
 
 /* Y = A W^T (+ bias) (then max(., 0) when relu == 1; NaN stays NaN). A n x in, W out x in, bias fp32[out] or NULL, Y
- * n x out in GPTQ_F32 or GPTQ_BF16. The sum of code products is a whole number and exact; it is converted to fp32 and
- * multiplied by the token's and then by the channel's scale, bias is added in fp32, and bf16 is rounded to at the end. */
+ * n x out in GPTQ_F32 or GPTQ_BF16. The sum S of code products is a whole number and exact. p = fp32(S) * a_scale, S and
+ * the product each rounded to fp32; y = p * w_scale + bias (0 for NULL) in one step, rounded once; bf16 is rounded to at the
+ * end. p has fp32's range: where |S| a_scale reaches 2^128 y is infinite whatever w_scale is, and below 2^-126 p loses
+ * bits. */
 size_t gptq_int8_matmul_workspace_bytes(int64_t n, int64_t in, int64_t out);
 int gptq_int8_matmul(const int8_t* a_codes, const float* a_scales, int64_t n, int64_t in, const int8_t* w_codes,
                      const float* w_scales, int64_t out, const float* bias, int relu, void* Y, int y_dtype, int64_t ld_y,

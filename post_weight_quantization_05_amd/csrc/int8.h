@@ -76,7 +76,8 @@ size_t rms_norm_grad_ws_bytes(int64_t n, int64_t d);
 hipError_t rms_norm_grad_launch(const NormGradArgs& a, int y_dtype, int h_dtype, hipStream_t stream);
 
 // A result from its exact sum: times the token's scale, times the channel's (plus bias, 0 for none, in the same step), no
-// less than low. Every kernel finishes by this, so results do not depend on the one that a size takes.
+// less than low. Every kernel finishes by this, so results do not depend on the one that a size takes. The first product
+// has fp32's range: it overflows for tokens of 2^105 and more only (a scale of 2^98 times a sum of 2^30).
 __device__ __forceinline__ float int8_result(float sum, float token, float channel, float bias, float low) {
   const float y = fmaf(sum * token, channel, bias);
   return y < low ? low : y;  // NaN stays

@@ -183,8 +183,8 @@ def int8_weight(result: QuantResult, stream=None) -> Int8Tensor:
 
 def int8_matmul(A: Int8Tensor, W: Int8Tensor, bias: torch.Tensor | None = None, relu: bool = False, dtype=torch.float32,
                 out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-    """Y = A W^T (+ bias, then ReLU when asked): A n x in, W out x in, Y n x out. Sums are exact; scales and bias are
-    applied in fp32."""
+    """Y = A W^T (+ bias, then ReLU when asked): A n x in, W out x in, Y n x out. Sums are exact; in fp32 they are multiplied
+    by the token's scale, and then by the channel's with bias added in the same step."""
     _int8(A, "A")
     c, n, d = A.codes, A.codes.shape[0], A.cols
     dev = c.get_device()
