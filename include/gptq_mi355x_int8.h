@@ -62,7 +62,7 @@ int gptq_int8_linear(const void* X, int x_dtype, int64_t n, int64_t in, int64_t 
                      void* ws, size_t ws_bytes, void* stream);
 
 /* Root-mean-square norm of h = X + R (h = X where R is NULL), weighted, in 8 bits:
- *   h is rounded to R's type and, where R is not NULL, written to H (that type, ld_h >= d);
+ *   h: the sum is rounded to fp32, then to R's type and, where R is not NULL, written to H (that type, ld_h >= d);
  *   rstd = 1 / sqrt(mean of h^2 + eps), sums in fp64, rounded to fp32 and written where rstd is not NULL (fp32[n]);
  *   u = h * weight, rounded to fp32 (weight: fp32[d]);
  *   GPTQ_NORM_INT8: u is quantized as by gptq_int8_quantize, and the row's scale is then multiplied by rstd;

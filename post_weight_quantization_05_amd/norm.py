@@ -55,9 +55,10 @@ def _vector(t: torch.Tensor, name: str, size: int, device: int) -> int:
 
 def rms_norm(X: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: torch.Tensor | None = None,
              fmt: str = "int8", out: torch.Tensor | None = None, stream=None) -> NormResult:
-    """h = X + residual, rounded to the residual's type; y = h / sqrt(mean h^2 + eps) * weight in 8 bits: integers with a
-    scale for each row ("int8", an Int8Tensor) or MX blocks ("e4m3", an MXTensor). X and residual n x d in bf16 or fp32,
-    weight fp32. out: where h goes, which may be the residual itself; without a residual h is X and nothing is written."""
+    """h = X + residual, rounded to fp32 and then to the residual's type; y = h / sqrt(mean h^2 + eps) * weight in 8 bits:
+    integers with a scale for each row ("int8", an Int8Tensor) or MX blocks ("e4m3", an MXTensor). X and residual n x d in
+    bf16 or fp32, weight fp32. out: where h goes, which may be the residual itself; without a residual h is X and nothing is
+    written."""
     try:
         code = _FMT[fmt]
     except (KeyError, TypeError):

@@ -1,5 +1,6 @@
 """The norm of a single token in place, in a column range of a wider buffer: the step of a decode loop whose stream lies among
-other state. Its results are those of the same row out of place, bit for bit, and the buffer around it stays as it was."""
+other state. Its results are those of the same row out of place, bit for bit, and the buffer around it stays as it was. And
+how the residual's sum is rounded."""
 import pytest
 import torch
 
@@ -59,3 +60,12 @@ def test_norm_of_single_tokens_in_place_replayed():
         assert torch.equal(h, eager) and torch.equal(res.y.codes, want.y.codes) and torch.equal(res.y.scales, want.y.scales)
     before[1:2, 40:552] = eager
     assert torch.equal(wide, before)
+
+
+@pytest.mark.parametrize("n", [1, 70])
+def test_residuals_sum_is_rounded_to_fp32_first(n):
+    """1 + (2^-8 + 2^-30) lies above the middle of two bf16 numbers, 1 and 1 + 2^-7, but rounds to it in fp32, and from there
+    to the even one of them."""
+    x = torch.full((n, 40), 2.0 ** -8 + 2.0 ** -30, device="cuda")
+    res = G.rms_norm(x, torch.ones(40, device="cuda"), residual=torch.ones((n, 40), dtype=torch.bfloat16, device="cuda"))
+    assert x[0, 0].item() == 2.0 ** -8 + 2.0 ** -30 and (res.h == 1).all()
