@@ -1,4 +1,5 @@
 """Results that the caller gives to the 8-bit integer operators and the norm (no GPU needed: the library is stood in for)."""
+import os
 import types
 
 import pytest
@@ -84,3 +85,18 @@ def test_gradient_refuses_a_number_for_the_weights_gradient_beside_a_given_resul
         with pytest.raises(ValueError):
             norm.rms_norm_grad(_t((40, 64)), _t((40, 64)), _t((40,)), _t((64,)), out=dx, weight_out=number, stream=STREAM)
     assert not calls
+
+
+@pytest.mark.skipif(not os.path.exists(_lib.LIB_PATH), reason="library not built")
+@pytest.mark.parametrize("n,d,out", [(20, 11008, 67), (64, 11008, 4096), (256, 28672, 8192), (11762, 10175, 448)])
+def test_sums_over_slices_need_their_workspace(n, d, out):
+    p = 4096  # an aligned address that is never read: every call below is refused
+    lib = _lib.load()
+    need = lib.gptq_int8_matmul_workspace_bytes(n, d, out)
+    assert need >= 2 * n * out * 4
+    for ws, have in ((None, need), (p + 16, need), (p, need - 1), (p, 0)):
+        assert lib.gptq_int8_matmul(p, p, n, d, p, p, out, None, 0, p, 0, out, ws, have, None) == _lib.GPTQ_ERR_WORKSPACE
+    whole = lib.gptq_int8_linear_workspace_bytes(n, d, out)
+    assert whole >= need + n * (-(-d // 128) * 128 + 4)
+    for ws, have in ((None, whole), (p + 16, whole), (p, whole - 1), (p, need)):
+        assert lib.gptq_int8_linear(p, 1, n, d, d, p, p, out, None, 0, p, 0, out, ws, have, None) == _lib.GPTQ_ERR_WORKSPACE
