@@ -402,15 +402,16 @@ struct TileProduct {
   // behind: transfers and stores (at least) that were issued since the next stage's transfers, or 0 if that is not known
   template <int BEHIND>
   __device__ __forceinline__ void deep_stage(int at, int nk, int behind) {
-    constexpr int F = MB + NB, W = (RING - 2) * PER + C2;
-    const uint32_t other = RING == 2 ? STAGE - slot : slot == (RING - 1) * STAGE ? 0u : slot + STAGE;
+    static_assert(RING == 2, "the stage after next comes into the buffer of the one being multiplied");
+    constexpr int F = MB + NB;
+    const uint32_t other = STAGE - slot;
     deep_step<0, 3 * F, 4 * F, 0, 0>(slot, slot);
     wait_and_barrier<63>();  // all waves have read all of the stage
-    const bool cross = at + RING == nk;
+    const bool cross = at + 2 == nk;
     a.mem.take_if(cross, an), b.mem.take_if(cross, bn);
     deep_step<1, 0, 0, 0, C1>(slot, slot);
     deep_step<2, 0, 0, C1, C2>(slot, slot);
-    wait_and_barrier_or<W, (W + BEHIND < 63 ? W + BEHIND : 63)>(behind);
+    wait_and_barrier_or<C2, (C2 + BEHIND < 63 ? C2 + BEHIND : 63)>(behind);
     deep_step<3, 0, 3 * F, C2, PER>(other, slot);
     slot = other;
   }
