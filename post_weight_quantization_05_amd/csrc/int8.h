@@ -35,8 +35,10 @@ hipError_t int8_linear_launch(const void* X, int x_dtype, int64_t n, int64_t ld_
 static inline bool int8_few(int64_t n, int64_t in, int64_t out) {
   return n <= 16 || (n <= 32 && in <= 4096 && out <= 4096);
 }
-// us of GPU time so / with a launch to quantize them, which also costs a call 3 us on the host: 1 x 4096 x 4096 7.3 / 8.3,
-// 8 x 4096 x 4096 10.5 / 8.9, 16 x 4096 x 4096 (too many) - / 9.4.
+// us of GPU time so / with a launch to quantize them, which also costs a call 3 us on the host: 1 x 4096 x 4096 7.1 / 8.4,
+// 4 x 4096 x 4096 8.6 / 8.7, 8 x 4096 x 4096 10.2 / 9.3, 16 x 4096 x 4096 (too many) - / 9.4. Every workgroup of 16 channels
+// quantizes all tokens anew, so wide layers lose by it what a launch does not cost: 8 x 4096 x 11008 19.3 / 16.3, 16 x 2048 x
+// 11008 16.1 / 12.1, and at 131072 channels 1 x 4096 93 / 93, 8 x 4096 135 / 117, 16 x 2048 123 / 80. The rule does not look at `out`.
 static inline bool int8_few_fused(int64_t n, int64_t in) {
   return n <= 16 && in >= 8 && (n <= 2 ? n : n <= 4 ? 4 : n <= 8 ? 8 : 16) * in <= 8 * 4096;
 }

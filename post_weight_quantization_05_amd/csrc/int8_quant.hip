@@ -69,7 +69,8 @@ __global__ __launch_bounds__(256) void k_int8_dequantize(const int8_t* __restric
   store8(Y, YBF16, row * ld + c, c, d, y);
 }
 
-// 16 bytes of a padded row a thread
+// 16 bytes of a padded row a thread, read one by one, since GPTQ's rows start at any byte; a layer is padded once (4096 x 4100
+// 25 us, 11008 x 4000 55; the copy's rate 7 and 18)
 __global__ __launch_bounds__(256) void k_int8_pad(const int8_t* __restrict__ codes, int d, int kp, int64_t total,
                                                   int8_t* __restrict__ padded) {
   const int per_row = kp / 16;

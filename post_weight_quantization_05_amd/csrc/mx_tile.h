@@ -244,8 +244,9 @@ struct TileProduct {
   // int8 in a ring of two holds the fragments of all four steps: those of the next stage's first three are read during the
   // last step and those of its fourth during its own first, so that a buffer is free for the stage after next from a stage's
   // second step on. Transfers then have up to six steps to land instead of four; shares as above, of the second, third and
-  // fourth step. us for 16384 x 4096 x 11008 with two steps' fragments 717, with these 672 (shares 4, 8, 12 of 16 with the
-  // rest in the next stage's first step 665, all in the second step 681). Small tiles with longer rings do without
+  // fourth step. us for 16384 x 4096 x 11008 with two steps' fragments 717, with these 672, all in the second step 681 (shares
+  // 4, 8, 12 of 16 with the rest in the next stage's first step 665, but that rest would be issued behind the last tile's
+  // stores, and what waits for it would wait for them: see `behind`). Small tiles with longer rings do without
   // (200 x 4096 x 4096 in a ring of four 11.0, with four steps' fragments and their second barrier 11.6).
   static constexpr bool DEEP = KA == K_INT8 && RING == 2;
   static constexpr int SETS = DEEP ? 4 : 2;

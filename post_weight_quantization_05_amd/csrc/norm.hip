@@ -39,7 +39,10 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
 }
 
 // RES: 0 no residual, 1 fp32, 2 bf16. A workgroup takes several rows in turn: the weight stays in registers, and the next row
-// is on its way while this one is reduced and written (rows of over 12288 columns leave no registers for that).
+// is on its way while this one is reduced and written (rows of over 12288 columns leave no registers for that). bf16 with a
+// bf16 residual, into int8 and E4M3: 8192 x 11008 123 and 128 us (the copy's rate 128), 8192 x 16384 210 and 184 (190), 2048 x
+// 65536 432 and 221 (190). Eight chunks a lane, rows of over 32768 columns, spill 39 to 54 registers into int8 and up to 8 into
+// E4M3; three chunks spill 6 in one form, fp32 with an fp32 residual into int8 (8192 x 11008 226 us, the copy's rate 237).
 template <bool XBF16, int RES, int FMT, int NCH, int LANES>
 __global__ __launch_bounds__(1024) void k_rms_norm(const NormArgs a, const RowShape rs, const double inv_d) {
   __shared__ RowShared shared;

@@ -12,8 +12,11 @@ namespace gptq {
 namespace {
 
 // HOLD: a row stays in registers between its sum and its gradient, and the next one is on its way meanwhile; rows of more than
-// 12288 columns are read again. Two and three chunks a lane take up to 209 registers: eight waves to a CU, with over 100 KB of
-// loads in flight between them (held to 128 registers 8192 x 11008 takes 500 us instead of 150).
+// 12288 columns are read again. Two and three chunks a lane take up to 205 registers: eight waves to a CU, with over 100 KB of
+// loads in flight between them (held to 128 registers 8192 x 11008 takes 500 us instead of 150). The longer rows' four and eight
+// chunks have up to sixteen waves and so 128 registers, of which their sums of dweight alone take 64 and 128: 138 to 174 and 466
+// to 541 registers are spilled, and updated in scratch memory for every row (8192 x 16384 in bf16 with dh 647 us, 2048 x 65536
+// 1097, the copy's rate 217 for both).
 template <bool YBF16, bool HBF16, bool DH, int NCH, int LANES>
 __global__ __launch_bounds__(NCH == 2 || NCH == 3 ? 512 : 1024) void k_rms_norm_grad(const NormGradArgs a, const RowShape rs) {
   constexpr bool HOLD = NCH <= 3;
